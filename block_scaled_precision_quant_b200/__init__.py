@@ -41,8 +41,10 @@ W_MXFP4, W_FP8BLK32, W_MXFP8 = 0, 1, 2
 W_A4W4 = 3  # MXFP4 weights with MXFP4 (packed E2M1) activations
 W_GRAD = 4  # E5M2 gradient codes x MXFP8 (E4M3) operand: the backward products
 W_NVFP4 = 5  # NVFP4 x NVFP4 (E2M1 with E4M3 scales per 16)
+W_INT8 = 6  # int8 x int8 with fp32 scales per token and per output channel
 BQ_ROUND_NEAREST, BQ_ROUND_STOCHASTIC = 0, 1
 BQ_FMT_E4M3, BQ_FMT_E5M2 = 0, 1
+BQ_GATE_SILU, BQ_GATE_GELU = 0, 1
 
 EXPORTS = (
     "bq_status_string", "bq_version", "bq_sf_bytes", "bq_act_quant", "bq_pack_weight_scales",
@@ -54,7 +56,9 @@ EXPORTS = (
     "bq_gemm_mxfp4_mxfp4_epilogue", "bq_grad_quant", "bq_quant_transposed", "bq_gemm_e5m2_mxfp8",
     "bq_gemm_e5m2_mxfp8_epilogue", "bq_grad_quant_dual", "bq_sf_bytes_nvfp4", "bq_act_quant_nvfp4",
     "bq_gemm_nvfp4_nvfp4", "bq_gemm_nvfp4_nvfp4_epilogue", "bq_selftest_wait_timeout",
-    "bq_debug_override_compute_capability",
+    "bq_debug_override_compute_capability", "bq_act_quant_int8", "bq_gemm_int8_int8",
+    "bq_gemm_int8_int8_epilogue", "bq_gemm_gated", "bq_gated_grad_quant",
+    "bq_ffn_plan",
 )
 
 
@@ -76,6 +80,11 @@ class Batch(ctypes.Structure):
                 ("stride_a_sf", ctypes.c_int64), ("stride_b", ctypes.c_int64),
                 ("stride_b_sf", ctypes.c_int64), ("stride_y", ctypes.c_int64),
                 ("stride_res", ctypes.c_int64)]
+
+
+class GatedEpilogue(ctypes.Structure):
+    _fields_ = [("alpha", ctypes.c_float), ("act", ctypes.c_int), ("gu_out", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("sf_out", ctypes.c_void_p)]
 
 
 class GemmConfig(ctypes.Structure):
@@ -161,6 +170,23 @@ def lib():
         L.bq_selftest_wait_timeout.restype = i32
         L.bq_debug_override_compute_capability.argtypes = [i32, i32]
         L.bq_debug_override_compute_capability.restype = i32
+        L.bq_act_quant_int8.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp]
+        L.bq_act_quant_int8.restype = i32
+        L.bq_gemm_int8_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp]
+        L.bq_gemm_int8_int8.restype = i32
+        L.bq_gemm_int8_int8_epilogue.argtypes = [
+            vp, vp, vp, vp, i64, i64, i64, vp, ctypes.POINTER(Epilogue), ctypes.POINTER(Batch),
+            ctypes.POINTER(GemmConfig), vp]
+        L.bq_gemm_int8_int8_epilogue.restype = i32
+        L.bq_gemm_gated.argtypes = [i32, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp,
+                                    ctypes.POINTER(GatedEpilogue), ctypes.POINTER(GemmConfig), vp]
+        L.bq_gemm_gated.restype = i32
+        L.bq_gated_grad_quant.argtypes = [vp, i64, vp, i64, i64, i64, i32, i32, ctypes.c_uint64,
+                                          vp, vp, vp, vp, vp, vp, vp]
+        L.bq_gated_grad_quant.restype = i32
+        L.bq_ffn_plan.argtypes = [i32, i32, i64, i64, i64, i64, ctypes.POINTER(GemmConfig), i32,
+                                  ctypes.POINTER(GemmConfig)]
+        L.bq_ffn_plan.restype = i32
         _lib = L
         return L
 
@@ -420,14 +446,19 @@ def gemm(weight_kind, a_q, a_sf, b, b_sf, M, N, K, y=None, bias=None, residual=N
     W_FP8BLK32, W_MXFP8 (E4M3 activations a_q [.., M, K]), W_A4W4 (packed
     E2M1 activations a_q [.., M, K/2] from act_quant_mxfp4), W_NVFP4 (packed
     E2M1 activations and weights with E4M3 scales per 16, from act_quant_nvfp4;
-    alpha = 1 / (g_a g_b) undoes the per-tensor scales) or W_GRAD (E5M2
-    gradient codes a_q [.., M, K], MXFP8 b).  batch: None or a dict with 'count' and byte
+    alpha = 1 / (g_a g_b) undoes the per-tensor scales), W_GRAD (E5M2
+    gradient codes a_q [.., M, K], MXFP8 b) or W_INT8 (gemm_int8_int8).  batch: None or a dict with 'count' and byte
     strides ('stride_a', 'stride_a_sf', 'stride_b', 'stride_b_sf', 'stride_y',
     'stride_res'; 0 broadcasts).  config: GemmConfig or None (auto).
     quantize_out: also return y quantized for the next GEMM (E4M3 codes
     [.., M, N] u8 and MMA-layout scales, exactly act_quant of y, written to
     q_out / sf_out when given); then returns (y or None, q, sf), with no bf16
     y written when write_y is False."""
+    if weight_kind == W_INT8:
+        if quantize_out or not write_y:
+            raise ValueError("the int8 product has no quantized output")
+        return gemm_int8_int8(a_q, a_sf, b, b_sf, M, N, K, y=y, bias=bias, residual=residual,
+                              alpha=alpha, act=act, batch=batch, config=config)
     torch = _torch()
     _need_cuda(a_q, a_sf, b, b_sf, bias, residual)
     count = 1 if batch is None else int(batch["count"])
@@ -541,6 +572,214 @@ def gemm_nvfp4_nvfp4(a_fp4, a_sf, b_fp4, b_sf, M, N, K, **kw):
 
 def gemm_e5m2_mxfp8(a_e5m2, a_sf, b_e4m3, b_sf, M, N, K, **kw):
     return gemm(W_GRAD, a_e5m2, a_sf, b_e4m3, b_sf, M, N, K, **kw)
+
+
+# -------------------------------------------- int8 and gated feed-forward ----
+
+def _device_index(torch, *ts):
+    """The calls run on the current device and stream: their tensors live there."""
+    here = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in ts:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("libbq works on CUDA tensors only")
+            if t.device.index != here:
+                raise ValueError("tensors must be on the current CUDA device")
+    return here
+
+
+def _need(t, dtype, numel, what):
+    if t is not None and (t.dtype != dtype or not t.is_contiguous() or t.numel() < numel):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of at least {numel} elements")
+
+
+def _need_rows(t, rows, cols, what):
+    """bf16 [rows, cols] with unit column stride (the row stride may exceed cols)."""
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a bf16 [{rows}, {cols}] tensor with unit column stride")
+    if str(t.dtype) != "torch.bfloat16":
+        raise ValueError(f"{what} must be bf16")
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor (one row has none of its own)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def ffn_plan(M, N, K, batch=1, config=None, num_sms=148, weight_kind=W_INT8,
+             gated=False) -> GemmConfig:
+    """The schedule of gemm_int8_int8 (W_INT8) or gemm_gated (gated=True), host-only:
+    every GemmConfig field resolved for a device with num_sms SMs."""
+    out = GemmConfig()
+    _check(lib().bq_ffn_plan(int(weight_kind), int(gated), M, N, K, batch,
+                             ctypes.byref(config) if config is not None else None, num_sms,
+                             ctypes.byref(out)), "bq_ffn_plan")
+    return out
+
+
+def act_quant_int8(x, q=None, scale=None, status=None):
+    """Per-row int8 quantization of a bf16 [M, K] CUDA tensor (row stride may
+    exceed K): returns (q int8 [M, K], scale fp32 [M]), q * scale ~ x.  Also the
+    quantizer of a weight [N, K] with one scale per output channel."""
+    torch = _torch()
+    _device_index(torch, x, q, scale, status)
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be a bf16 [M, K] tensor with unit column stride")
+    M, K = x.shape
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _need(q, torch.int8, M * K, "q")
+    _need(scale, torch.float32, M, "scale")
+    _check(lib().bq_act_quant_int8(x.data_ptr(), M, K, _ld(x), q.data_ptr(), scale.data_ptr(),
+                                   _ptr(status), _stream()), "bq_act_quant_int8")
+    return q, scale
+
+
+def gemm_int8_int8(a_q, a_scale, b, b_scale, M, N, K, y=None, bias=None, residual=None, alpha=1.0,
+                   act=BQ_ACT_NONE, batch=None, config=None):
+    """y = bf16(act(alpha * a_scale[m] * b_scale[n] * (A B^T) + bias) + residual) of
+    int8 codes a_q [.., M, K] and b [.., N, K] with fp32 scales per token and per
+    output channel (act_quant_int8).  batch: as in gemm; its scale strides
+    step the fp32 scales.  config: GemmConfig or None (auto)."""
+    torch = _torch()
+    _device_index(torch, a_q, a_scale, b, b_scale, y, bias, residual)
+    count, sa, ssa, sb, ssb, sy, sr = 1, 0, 0, 0, 0, 0, 0
+    if batch is not None:
+        count = int(batch["count"])
+        sa, ssa, sb, ssb, sy, sr = (int(batch.get(k, 0)) for k in (
+            "stride_a", "stride_a_sf", "stride_b", "stride_b_sf", "stride_y", "stride_res"))
+    more = max(count - 1, 0) if M and N else 0
+    _need(a_q, torch.int8, M * K + more * sa, "a_q")
+    _need(b, torch.int8, N * K + more * sb, "b")
+    _need(a_scale, torch.float32, M + more * (ssa // 4), "a_scale")
+    _need(b_scale, torch.float32, N + more * (ssb // 4), "b_scale")
+    _need(bias, torch.bfloat16, N, "bias")
+    if y is None:
+        y = torch.empty((M, N) if batch is None else (count, M, N), dtype=torch.bfloat16,
+                        device=a_q.device)
+    _need(y, torch.bfloat16, M * N + more * (sy // 2), "y")
+    ld = 0
+    if residual is not None:
+        if batch is None:
+            _need_rows(residual, M, N, "residual")
+            ld = _ld(residual)
+        else:
+            if residual.dtype != torch.bfloat16 or residual.dim() < 2 or residual.stride(-1) != 1:
+                raise ValueError("residual must be bf16 with unit column stride")
+            ld = residual.stride(-2)
+    plain = (bias is None and residual is None and alpha == 1.0 and act == BQ_ACT_NONE
+             and batch is None and config is None)
+    if plain:
+        _check(lib().bq_gemm_int8_int8(a_q.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
+                                       b_scale.data_ptr(), M, N, K, y.data_ptr(), _stream()),
+               "bq_gemm_int8_int8")
+        return y
+    epi = Epilogue(bias.data_ptr() if bias is not None else None,
+                   residual.data_ptr() if residual is not None else None, ld, float(alpha),
+                   int(act), None, None)
+    bt = None if batch is None else ctypes.byref(Batch(count, sa, ssa, sb, ssb, sy, sr))
+    _check(lib().bq_gemm_int8_int8_epilogue(
+        a_q.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), M, N, K,
+        y.data_ptr(), ctypes.byref(epi), bt,
+        None if config is None else ctypes.byref(config), _stream()),
+        "bq_gemm_int8_int8_epilogue")
+    return y
+
+
+def gemm_gated(weight_kind, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, M, N, K, y=None,
+               act=BQ_GATE_SILU, alpha=1.0, keep_projections=False, gu=None, quantize_out=False,
+               write_y=True, q_out=None, sf_out=None, config=None):
+    """h = bf16(act(g) * u) with g = alpha A Wg^T and u = alpha A Wu^T, the gated
+    feed-forward block up to its hidden row, in one kernel.  weight_kind W_MXFP4,
+    W_FP8BLK32 or W_MXFP8 (E4M3 activations and MMA-layout scales, as in gemm) or
+    W_INT8 (int8 codes and fp32 scales, as in gemm_int8_int8); both weights
+    [N, K].  keep_projections (or gu given): also return [g | u] bf16 [M, 2 N] for
+    gated_grad_quant.  quantize_out: also return h quantized for the down
+    projection (E4M3 codes and MMA-layout scales, exactly act_quant of h); no bf16
+    h is written when write_y is False.  Returns h, or a tuple (h or None, [q, sf],
+    [gu]) when quantize_out or keep_projections ask for more."""
+    torch = _torch()
+    _device_index(torch, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, y, gu, q_out, sf_out)
+    if not write_y and not quantize_out:
+        raise ValueError("write_y=False needs quantize_out=True")
+    dev = a_q.device
+    if weight_kind == W_INT8:
+        _need(a_q, torch.int8, M * K, "a_q")
+        _need(a_sf, torch.float32, M, "a_sf")
+        for w, s in ((b_gate, gate_sf), (b_up, up_sf)):
+            _need(w, torch.int8, N * K, "weights")
+            _need(s, torch.float32, N, "weight scales")
+    else:
+        _need(a_q, torch.uint8, M * K, "a_q")
+        _need(a_sf, torch.uint8, sf_bytes(M, K), "a_sf")
+        nb = N * K // 2 if weight_kind == W_MXFP4 else N * K
+        for w, s in ((b_gate, gate_sf), (b_up, up_sf)):
+            _need(w, torch.uint8, nb, "weights")
+            _need(s, torch.uint8, sf_bytes(N, K), "weight scales")
+    if not write_y:
+        y = None
+    elif y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    if keep_projections and gu is None:
+        gu = torch.empty((M, 2 * N), dtype=torch.bfloat16, device=dev)
+    if quantize_out:
+        if q_out is None:
+            q_out = torch.empty((M, N), dtype=torch.uint8, device=dev)
+        if sf_out is None:
+            sf_out = torch.empty((max(sf_bytes(M, N), 1),), dtype=torch.uint8, device=dev)
+        _need(q_out, torch.uint8, M * N, "q_out")
+        _need(sf_out, torch.uint8, sf_bytes(M, N), "sf_out")
+    else:
+        q_out = sf_out = None
+    _need(y, torch.bfloat16, M * N, "y")
+    _need(gu, torch.bfloat16, 2 * M * N, "gu")
+    epi = GatedEpilogue(float(alpha), int(act), None if gu is None else gu.data_ptr(),
+                        None if q_out is None else q_out.data_ptr(),
+                        None if sf_out is None else sf_out.data_ptr())
+    _check(lib().bq_gemm_gated(
+        int(weight_kind), a_q.data_ptr(), a_sf.data_ptr(), b_gate.data_ptr(), gate_sf.data_ptr(),
+        b_up.data_ptr(), up_sf.data_ptr(), M, N, K, None if y is None else y.data_ptr(),
+        ctypes.byref(epi), None if config is None else ctypes.byref(config), _stream()),
+        "bq_gemm_gated")
+    if not quantize_out and gu is None:
+        return y
+    return (y,) + ((q_out, sf_out) if quantize_out else ()) + ((gu,) if gu is not None else ())
+
+
+def gated_grad_quant(dh, gu, act=BQ_GATE_SILU, stochastic=False, seed=0, out=None, d=None,
+                     status=None):
+    """Backward pass of h = act(g) * u: d = [dh * u * act'(g) | dh * act(g)] [M, 2 N]
+    from dh bf16 [M, N] and gu = [g | u] bf16 [M, 2 N], quantized to E5M2 along
+    both dimensions as grad_quant_dual(d) does.  Returns (q_row [M, 2 N], sf_row, q_t
+    [2 N, M], sf_t); d (bf16 [M, 2 N]) is written when given."""
+    torch = _torch()
+    q_row = sf_row = q_t = sf_t = None
+    if out is not None:
+        q_row, sf_row, q_t, sf_t = out
+    _device_index(torch, dh, gu, q_row, sf_row, q_t, sf_t, d, status)
+    if dh.dim() != 2:
+        raise ValueError("dh must be a bf16 [M, N] tensor")
+    M, N = dh.shape
+    _need_rows(dh, M, N, "dh")
+    _need_rows(gu, M, 2 * N, "gu")
+    n_row, n_t = max(sf_bytes(M, 2 * N), 1), max(sf_bytes(2 * N, M) if M else 1, 1)
+    if out is None:
+        u8 = dict(dtype=torch.uint8, device=dh.device)
+        q_row, sf_row = torch.empty((M, 2 * N), **u8), torch.empty((n_row,), **u8)
+        q_t, sf_t = torch.empty((2 * N, M), **u8), torch.empty((n_t,), **u8)
+    _need(q_row, torch.uint8, 2 * M * N, "q_row")
+    _need(q_t, torch.uint8, 2 * M * N, "q_t")
+    _need(sf_row, torch.uint8, n_row, "sf_row")
+    _need(sf_t, torch.uint8, n_t, "sf_t")
+    _need(d, torch.bfloat16, 2 * M * N, "d")
+    _check(lib().bq_gated_grad_quant(
+        dh.data_ptr(), _ld(dh), gu.data_ptr(), _ld(gu), M, N, int(act),
+        BQ_ROUND_STOCHASTIC if stochastic else BQ_ROUND_NEAREST, int(seed) & (2 ** 64 - 1),
+        q_row.data_ptr(), sf_row.data_ptr(), q_t.data_ptr(), sf_t.data_ptr(),
+        None if d is None else d.data_ptr(), _ptr(status), _stream()), "bq_gated_grad_quant")
+    return q_row, sf_row, q_t, sf_t
 
 
 config = _config

@@ -13,6 +13,7 @@
 
 #include "act_quant.cuh"
 #include "bq.h"
+#include "bq_host.cuh"
 #include "gemm_bs.cuh"
 #include "gemm_pair.cuh"
 
@@ -795,6 +796,25 @@ int gemm_entry(WeightKind wk, const void* a_q, const void* a_sf, const void* b, 
 }
 
 }  // namespace
+
+// What the library's other translation units need of this one.
+namespace bqh {
+
+int current_device(Device* d) {
+  DevInfo* info = nullptr;
+  const int st = ::current_device(&info);
+  if (st != BQ_OK) return st;
+  d->index = static_cast<int>(info - g_dev);
+  d->num_sms = info->num_sms;
+  d->err = info->err_ptr;
+  return BQ_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  return get_encoder() == BQ_OK ? g_encode : nullptr;
+}
+
+}  // namespace bqh
 
 // ================================================================== C ABI ==
 

@@ -1,0 +1,406 @@
+// bq_ffn.cu -- host side of the int8 and gated feed-forward entry points of
+// include/bq.h: argument checks, tensor maps, schedules and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "bq.h"
+#include "bq_host.cuh"
+#include "gated_grad.cuh"
+#include "lin_swap.cuh"
+#include "quant_i8.cuh"
+
+namespace {
+
+using bqh::aligned;
+using bqh::Device;
+
+// Weight kinds of these entry points (the GEMMs' numbers, and 6 for int8).
+enum Kind { kMxfp4 = 0, kFp8Blk32 = 1, kMxfp8 = 2, kInt8 = 6 };
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int launch_status() { return cudaGetLastError() == cudaSuccess ? BQ_OK : BQ_ERR_CUDA; }
+
+// Launch with programmatic dependence on the kernel before, in clusters of
+// `cluster` blocks.
+template <class... P, class... A>
+int launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster,
+           bq_stream_t stream, A... args) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(static_cast<unsigned>(threads));
+  lc.dynamicSmemBytes = smem;
+  lc.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&lc, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return BQ_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+// A K-major operand of one byte (E2M1: half a byte) per code as (K, rows,
+// batch): boxes of 128 codes x box_rows rows, 128-byte swizzle, zeros outside.
+int operand_map(CUtensorMap* m, const void* base, bool fp4, int64_t K, int64_t rows, int64_t batch,
+                int64_t batch_bytes, int64_t box_rows) {
+  auto encode = bqh::tensor_map_encoder();
+  if (!encode) return BQ_ERR_CUDA;
+  const int64_t row_bytes = fp4 ? K / 2 : K;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {
+      static_cast<cuuint64_t>(row_bytes),
+      static_cast<cuuint64_t>(batch > 1 ? batch_bytes : row_bytes * rows)};
+  const cuuint32_t box[3] = {128u, static_cast<cuuint32_t>(box_rows), 1u};
+  const cuuint32_t step[3] = {1u, 1u, 1u};
+  const CUresult r = encode(
+      m, fp4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+      const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? BQ_OK : BQ_ERR_ALIGN;
+}
+
+// ---------------------------------------------------------------- schedule --
+
+struct Plan {
+  int bn = 0;      // activation rows of a tile
+  int splits = 1;  // K slices (CTAs of a cluster)
+  int64_t tiles_p = 0, tiles_q = 0, tiles = 0;
+  int kt = 0;
+};
+
+constexpr int kMaxSplit = 8;  // portable cluster size
+
+int check_config(const bq_gemm_config* cfg) {
+  if (!cfg) return BQ_OK;
+  const bq_gemm_config& c = *cfg;
+  if (c.block_n != 0 && c.block_n != 32 && c.block_n != 64 && c.block_n != 128)
+    return BQ_ERR_INVALID;
+  if (c.split_k < 0 || c.split_k > kMaxSplit || c.swap_ab < -1 || c.swap_ab == 0 ||
+      c.swap_ab > 1 || (c.split_mode != BQ_SPLIT_AUTO && c.split_mode != BQ_SPLIT_CLUSTER) ||
+      c.k_chunks < 0 || c.k_chunks > 1 || c.cta_pair < 0 || c.cta_pair > 1)
+    return BQ_ERR_INVALID;
+  return BQ_OK;
+}
+
+int make_plan(Kind kind, int64_t M, int64_t N, int64_t K, int64_t batch,
+              const bq_gemm_config* cfg, int num_sms, Plan* p) {
+  const bq_gemm_config c = cfg ? *cfg : bq_gemm_config{0, 0, -1, BQ_SPLIT_AUTO, 0, 0};
+  // MX tiles start at the first row of a scale atom (lin_swap.cuh)
+  if (kind != kInt8 && c.block_n != 0 && c.block_n < 128 && M > c.block_n) return BQ_ERR_INVALID;
+  p->kt = static_cast<int>(ceil_div(K, 128));
+  p->bn = c.block_n ? c.block_n : (M <= 32 ? 32 : M <= 64 ? 64 : 128);
+  p->tiles_p = ceil_div(N, 128);
+  p->tiles_q = ceil_div(M, p->bn);
+  p->tiles = p->tiles_p * p->tiles_q * batch;
+  int s = c.split_k;
+  if (s == 0) {
+    s = 1;
+    while (s < kMaxSplit && p->tiles * (s + 1) <= num_sms && p->kt / (s + 1) >= 2) ++s;
+  }
+  p->splits = std::min(s, p->kt);
+  if (p->tiles * p->splits > 0x7FFFFFFF) return BQ_ERR_SHAPE;
+  return BQ_OK;
+}
+
+// ---------------------------------------------------------------- launches --
+
+template <int BN, bool I8, bool GATED>
+int launch_swap(const Plan& pl, const CUtensorMap& w0, const CUtensorMap& w1,
+                const CUtensorMap& ta, const bq::FfnArgs& a, int dev, bq_stream_t stream) {
+  using L = bq::SwapSmem<BN, I8, GATED>;
+  auto kern = bq::lin_swap_kernel<BN, I8, GATED>;
+  static bool ready[bqh::kMaxDevices] = {};
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
+        cudaSuccess)
+      return BQ_ERR_CUDA;
+    ready[dev] = true;
+  }
+  return launch(kern, dim3(static_cast<unsigned>(pl.tiles * pl.splits)), bq::kSwapThreads,
+                L::kBytes, pl.splits, stream, w0, w1, ta, a);
+}
+
+template <bool I8, bool GATED>
+int run_swap(const Plan& pl, const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& ta,
+             const bq::FfnArgs& a, int dev, bq_stream_t stream) {
+  switch (pl.bn) {
+    case 32: return launch_swap<32, I8, GATED>(pl, w0, w1, ta, a, dev, stream);
+    case 64: return launch_swap<64, I8, GATED>(pl, w0, w1, ta, a, dev, stream);
+    default: return launch_swap<128, I8, GATED>(pl, w0, w1, ta, a, dev, stream);
+  }
+}
+
+// What a call of either operator brings.  w[1] is NULL for the plain product.
+struct Call {
+  Kind kind;
+  const void *a, *a_sf;
+  const void *w[2], *w_sf[2];
+  int64_t M, N, K;
+  bq_batch batch{1, 0, 0, 0, 0, 0, 0};
+};
+
+// Sums of int8 products stay below 2^31: K 128 128 < 2^31.
+constexpr int64_t kMaxInt8K = (int64_t{1} << 17) - 1;
+
+// Checks of the operands and of the sizes.
+int check_operands(const Call& c) {
+  const bool i8 = c.kind == kInt8;
+  if (c.M < 0 || c.N < 0 || c.K <= 0 || c.K % (i8 ? 16 : 32) != 0 || c.N % 8 != 0 ||
+      c.M > 0x7FFFFFFF || c.N > 0x7FFFFFFF || c.K > 0x7FFFFFFF || (i8 && c.K > kMaxInt8K) ||
+      (c.kind == kMxfp4 && c.K % 128 != 0) || c.batch.count < 0 || c.batch.count > 65535)
+    return BQ_ERR_SHAPE;
+  return BQ_OK;
+}
+
+int check_pointers(const Call& c, bool gated) {
+  const bool i8 = c.kind == kInt8;
+  if (!c.a || !c.a_sf) return BQ_ERR_NULL;
+  for (int w = 0; w < (gated ? 2 : 1); ++w)
+    if (!c.w[w] || !c.w_sf[w]) return BQ_ERR_NULL;
+  if (!aligned(c.a, 16) || !aligned(c.a_sf, i8 ? 4 : 16)) return BQ_ERR_ALIGN;
+  for (int w = 0; w < (gated ? 2 : 1); ++w)
+    if (!aligned(c.w[w], c.kind == kMxfp4 ? 32 : 16) || !aligned(c.w_sf[w], i8 ? 4 : 16))
+      return BQ_ERR_ALIGN;
+  return BQ_OK;
+}
+
+void operand_args(const Call& c, bq::FfnArgs* g) {
+  const bool i8 = c.kind == kInt8;
+  g->M = static_cast<int>(c.M);
+  g->N = static_cast<int>(c.N);
+  g->K = static_cast<int>(c.K);
+  g->batch = static_cast<int>(c.batch.count);
+  g->sf_katoms = static_cast<int>(ceil_div(c.K, 128));
+  g->sf_a_bands = static_cast<int>(ceil_div(c.M, 128));
+  g->w_tile_bytes = 128 * 128 / (c.kind == kMxfp4 ? 2 : 1);
+  g->fmt_a = bq::kFmtE4M3;
+  g->fmt_w = c.kind == kMxfp4 ? bq::kFmtE2M1 : bq::kFmtE4M3;
+  if (i8) {
+    g->sa = static_cast<const float*>(c.a_sf);
+    g->sa_bstride = c.batch.stride_a_sf / 4;
+    g->sw_bstride = c.batch.stride_b_sf / 4;
+  } else {
+    g->sf_a = static_cast<const uint8_t*>(c.a_sf);
+  }
+  for (int w = 0; w < 2; ++w) {
+    if (i8)
+      g->sw[w] = static_cast<const float*>(c.w_sf[w]);
+    else
+      g->sf_w[w] = static_cast<const uint8_t*>(c.w_sf[w]);
+  }
+  g->ldy = c.N;
+  g->y_bstride = c.batch.stride_y / 2;
+  g->res_bstride = c.batch.stride_res / 2;
+  g->p_batched = c.batch.count > 1 && c.batch.stride_b != 0;
+  g->q_batched = c.batch.count > 1 && c.batch.stride_a != 0;
+}
+
+// The call after its argument checks.
+int run(const Call& c, bool gated, bool empty, const bq_gemm_config* cfg, bq::FfnArgs* g,
+        bq_stream_t stream) {
+  int st = check_config(cfg);
+  if (st != BQ_OK) return st;
+  Device dev;
+  st = bqh::current_device(&dev);
+  if (st != BQ_OK || empty) return st;
+  Plan pl;
+  st = make_plan(c.kind, c.M, c.N, c.K, c.batch.count, cfg, dev.num_sms, &pl);
+  if (st != BQ_OK) return st;
+  const bool i8 = c.kind == kInt8, fp4 = c.kind == kMxfp4;
+  operand_args(c, g);
+  g->err = dev.err;
+  g->kt_total = pl.kt;
+  g->splits = pl.splits;
+  g->tiles_p = static_cast<int>(pl.tiles_p);
+  g->tiles_q = static_cast<int>(pl.tiles_q);
+  // One tile over all rows: its box ends at the last row (a box whose trailing
+  // rows all lie outside the tensor copies slower).
+  g->q_box_rows =
+      pl.tiles_q == 1 ? static_cast<int>(std::min<int64_t>(pl.bn, (c.M + 7) / 8 * 8)) : pl.bn;
+  CUtensorMap ta, tw[2];
+  st = operand_map(&ta, c.a, false, c.K, c.M, g->q_batched ? c.batch.count : 1, c.batch.stride_a,
+                   g->q_box_rows);
+  for (int w = 0; st == BQ_OK && w < (gated ? 2 : 1); ++w)
+    st = operand_map(&tw[w], c.w[w], fp4, c.K, c.N, g->p_batched ? c.batch.count : 1,
+                     c.batch.stride_b, 128);
+  if (st != BQ_OK) return st;
+  if (!gated) return run_swap<true, false>(pl, tw[0], tw[0], ta, *g, dev.index, stream);
+  return i8 ? run_swap<true, true>(pl, tw[0], tw[1], ta, *g, dev.index, stream)
+            : run_swap<false, true>(pl, tw[0], tw[1], ta, *g, dev.index, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int bq_act_quant_int8(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, void* q_s8,
+                      float* scale, int* d_status, bq_stream_t stream) {
+  if (M < 0 || M > 0x7FFFFFFF || K <= 0 || K % 16 != 0 || ldx < K) return BQ_ERR_SHAPE;
+  if (M > 0) {
+    if (!x_bf16 || !q_s8 || !scale) return BQ_ERR_NULL;
+    if (!aligned(x_bf16, 16) || ldx % 8 != 0 || !aligned(q_s8, 16) || !aligned(scale, 4))
+      return BQ_ERR_ALIGN;
+  }
+  Device dev;
+  const int st = bqh::current_device(&dev);
+  if (st != BQ_OK || M == 0) return st;
+  return launch(bq::i8_quant_kernel, dim3(static_cast<unsigned>(M)), 256, 0, 1, stream,
+                static_cast<const __nv_bfloat16*>(x_bf16), M, K, ldx,
+                static_cast<uint8_t*>(q_s8), scale, d_status);
+}
+
+int bq_gemm_int8_int8_epilogue(const void* a_s8, const float* a_scale, const void* b_s8,
+                               const float* b_scale, int64_t M, int64_t N, int64_t K, void* y_bf16,
+                               const bq_epilogue* epi, const bq_batch* batch,
+                               const bq_gemm_config* cfg, bq_stream_t stream) {
+  Call c{kInt8, a_s8, a_scale, {b_s8, nullptr}, {b_scale, nullptr}, M, N, K};
+  if (batch) c.batch = *batch;
+  int st = check_operands(c);
+  if (st != BQ_OK) return st;
+  const bool empty = M == 0 || N == 0 || c.batch.count == 0;
+  if (!empty) {
+    if ((st = check_pointers(c, false)) != BQ_OK) return st;
+    if (!y_bf16) return BQ_ERR_NULL;
+    if (!aligned(y_bf16, 16)) return BQ_ERR_ALIGN;
+  }
+  bq::FfnArgs g;
+  memset(&g, 0, sizeof(g));
+  g.alpha = 1.0f;
+  if (epi) {
+    if (epi->act != BQ_ACT_NONE && epi->act != BQ_ACT_GELU) return BQ_ERR_INVALID;
+    if (epi->q_out || epi->sf_out) return BQ_ERR_INVALID;
+    if (epi->bias && !aligned(epi->bias, 16)) return BQ_ERR_ALIGN;
+    if (epi->residual && (!aligned(epi->residual, 16) || epi->ld_residual % 8 != 0 ||
+                          epi->ld_residual < N))
+      return BQ_ERR_ALIGN;
+    g.alpha = epi->alpha;
+    g.act = epi->act;
+    g.bias = static_cast<const __nv_bfloat16*>(epi->bias);
+    g.res = static_cast<const __nv_bfloat16*>(epi->residual);
+    g.ldres = epi->ld_residual;
+  }
+  if (c.batch.count > 1) {
+    const bq_batch& b = c.batch;
+    if (b.stride_a < 0 || b.stride_a_sf < 0 || b.stride_b < 0 || b.stride_b_sf < 0 ||
+        b.stride_y <= 0 || b.stride_res < 0)
+      return BQ_ERR_SHAPE;
+    if (b.stride_a % 16 || b.stride_b % 16 || b.stride_a_sf % 4 || b.stride_b_sf % 4 ||
+        b.stride_y % 16 || b.stride_res % 16)
+      return BQ_ERR_ALIGN;
+  }
+  g.y = static_cast<__nv_bfloat16*>(y_bf16);
+  return run(c, false, empty, cfg, &g, stream);
+}
+
+int bq_gemm_int8_int8(const void* a_s8, const float* a_scale, const void* b_s8,
+                      const float* b_scale, int64_t M, int64_t N, int64_t K, void* y_bf16,
+                      bq_stream_t stream) {
+  return bq_gemm_int8_int8_epilogue(a_s8, a_scale, b_s8, b_scale, M, N, K, y_bf16, nullptr,
+                                    nullptr, nullptr, stream);
+}
+
+int bq_gemm_gated(int weight_kind, const void* a_q, const void* a_sf, const void* b_gate,
+                  const void* gate_sf, const void* b_up, const void* up_sf, int64_t M, int64_t N,
+                  int64_t K, void* h_bf16, const bq_gated_epilogue* epi,
+                  const bq_gemm_config* cfg, bq_stream_t stream) {
+  if (weight_kind != kMxfp4 && weight_kind != kFp8Blk32 && weight_kind != kMxfp8 &&
+      weight_kind != kInt8)
+    return BQ_ERR_INVALID;
+  const Call c{static_cast<Kind>(weight_kind), a_q, a_sf, {b_gate, b_up}, {gate_sf, up_sf},
+               M, N, K};
+  int st = check_operands(c);
+  if (st != BQ_OK) return st;
+  const bq_gated_epilogue e = epi ? *epi : bq_gated_epilogue{1.0f, BQ_GATE_SILU, nullptr, nullptr,
+                                                             nullptr};
+  if (e.act != BQ_GATE_SILU && e.act != BQ_GATE_GELU) return BQ_ERR_INVALID;
+  if ((e.q_out || e.sf_out) && N % 32 != 0) return BQ_ERR_SHAPE;
+  if ((e.q_out != nullptr) != (e.sf_out != nullptr)) return BQ_ERR_NULL;
+  const bool empty = M == 0 || N == 0;
+  if (!empty) {
+    if ((st = check_pointers(c, true)) != BQ_OK) return st;
+    if (!h_bf16 && !e.q_out) return BQ_ERR_NULL;
+    if (!aligned(h_bf16, 16) || !aligned(e.gu_out, 16) || !aligned(e.q_out, 16) ||
+        !aligned(e.sf_out, 4))
+      return BQ_ERR_ALIGN;
+  }
+  bq::FfnArgs g;
+  memset(&g, 0, sizeof(g));
+  g.alpha = e.alpha;
+  g.act = e.act;
+  g.y = static_cast<__nv_bfloat16*>(h_bf16);
+  g.gu = static_cast<__nv_bfloat16*>(e.gu_out);
+  g.q_out = static_cast<uint8_t*>(e.q_out);
+  g.sf_out = static_cast<uint8_t*>(e.sf_out);
+  return run(c, true, empty, cfg, &g, stream);
+}
+
+int bq_gated_grad_quant(const void* dh_bf16, int64_t ld_dh, const void* gu_bf16, int64_t ld_gu,
+                        int64_t M, int64_t N, int act, int rounding, uint64_t seed, void* q_row,
+                        void* sf_row, void* q_t, void* sf_t, void* d_bf16, int* d_status,
+                        bq_stream_t stream) {
+  if (act != BQ_GATE_SILU && act != BQ_GATE_GELU) return BQ_ERR_INVALID;
+  if (rounding != BQ_ROUND_NEAREST && rounding != BQ_ROUND_STOCHASTIC) return BQ_ERR_INVALID;
+  if (M < 0 || M % 32 != 0 || N <= 0 || N % 32 != 0 || ld_dh < N || ld_gu < 2 * N)
+    return BQ_ERR_SHAPE;
+  const int64_t groups = ceil_div(M, 128) * 4, tiles = ceil_div(N, 64);
+  if (groups > 0x7FFFFFFF || ceil_div(tiles, 8) > 65535) return BQ_ERR_SHAPE;
+  if (M > 0) {
+    if (!dh_bf16 || !gu_bf16 || !q_row || !sf_row || !q_t || !sf_t) return BQ_ERR_NULL;
+    if (!aligned(dh_bf16, 16) || !aligned(gu_bf16, 16) || ld_dh % 8 != 0 || ld_gu % 8 != 0 ||
+        !aligned(q_row, 16) || !aligned(q_t, 16) || !aligned(d_bf16, 16))
+      return BQ_ERR_ALIGN;
+  }
+  Device dev;
+  const int st = bqh::current_device(&dev);
+  if (st != BQ_OK || M == 0) return st;
+  const bool sr = rounding == BQ_ROUND_STOCHASTIC;
+  auto kern = act == BQ_GATE_SILU ? (sr ? bq::gated_grad_kernel<bq::kGateSilu, true>
+                                        : bq::gated_grad_kernel<bq::kGateSilu, false>)
+                                  : (sr ? bq::gated_grad_kernel<bq::kGateGelu, true>
+                                        : bq::gated_grad_kernel<bq::kGateGelu, false>);
+  return launch(kern, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(ceil_div(tiles, 8))),
+                256, 0, 1, stream, static_cast<const __nv_bfloat16*>(dh_bf16), ld_dh,
+                static_cast<const __nv_bfloat16*>(gu_bf16), ld_gu, M, N, tiles,
+                static_cast<uint8_t*>(q_row), static_cast<uint8_t*>(sf_row),
+                static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(sf_t),
+                static_cast<__nv_bfloat16*>(d_bf16), d_status, seed);
+}
+
+int bq_ffn_plan(int weight_kind, int gated, int64_t M, int64_t N, int64_t K, int64_t batch,
+                const bq_gemm_config* cfg, int num_sms, bq_gemm_config* out) {
+  if (!out) return BQ_ERR_NULL;
+  if (weight_kind != kInt8 && (!gated || weight_kind < kMxfp4 || weight_kind > kMxfp8))
+    return BQ_ERR_INVALID;
+  Call c{static_cast<Kind>(weight_kind), nullptr, nullptr, {nullptr, nullptr}, {nullptr, nullptr},
+         M, N, K};
+  c.batch.count = batch;
+  if (M <= 0 || N <= 0 || batch <= 0 || num_sms < 1) return BQ_ERR_SHAPE;
+  int st = check_operands(c);
+  if (st == BQ_OK) st = check_config(cfg);
+  Plan pl;
+  if (st == BQ_OK) st = make_plan(c.kind, M, N, K, batch, cfg, num_sms, &pl);
+  if (st != BQ_OK) return st;
+  out->block_n = pl.bn;
+  out->split_k = pl.splits;
+  out->swap_ab = 1;
+  out->split_mode = pl.splits > 1 ? BQ_SPLIT_CLUSTER : BQ_SPLIT_AUTO;
+  out->k_chunks = 1;
+  out->cta_pair = 1;
+  return BQ_OK;
+}
+
+}  // extern "C"

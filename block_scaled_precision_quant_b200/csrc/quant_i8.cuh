@@ -1,0 +1,73 @@
+// quant_i8.cuh -- per-token int8 quantization of bf16 rows.
+//
+//   amax = max(max_k |x[m, k]|, 2^-64);  scale[m] = fp32(amax / 127)
+//   q = the integer nearest 127 x / amax, ties to even (in -127 .. 127)
+//
+// The quotient's rounding is exact.  Let c = fp32(127 / amax) and y = fp32(x c):
+// two roundings, so y is within 2^-23 (relative) of n = 127 x / amax.  A tie
+// (n = k + 1/2, k < 127) has at most 8 significant bits.  With x = X 2^i and
+// amax = A 2^j, X and A below 2^8, any other n is at least 1 / (2 A) of a unit
+// of 2^(i - j) away from a tie, that is 2^-17 relative.  Rounding y to 18
+// bits moves it by at most 2^-18 relative: ties land on themselves, nothing
+// else does.  Then the conversion's own round to nearest even decides.  The
+// floor of amax is a power of two so that A stays short.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "bq_ptx.cuh"
+#include "mx_quant.cuh"
+
+namespace bq {
+
+// Int8 code (low byte) of the bf16 value whose fp32 bits are `bits`.
+__device__ __forceinline__ int i8_code(uint32_t bits, float c) {
+  const uint32_t y = __float_as_uint(__fmul_rn(__uint_as_float(bits), c));
+  return __float2int_rn(__uint_as_float((y + 32u) & ~63u));
+}
+
+// Four codes of two words of bf16 pairs.
+__device__ __forceinline__ uint32_t i8_codes4(uint32_t w0, uint32_t w1, float c) {
+  const int a = i8_code(w0 << 16, c), b = i8_code(w0 & 0xFFFF0000u, c);
+  const int d = i8_code(w1 << 16, c), e = i8_code(w1 & 0xFFFF0000u, c);
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(d, e, 0x0040), 0x5410);
+}
+
+// One block per row; the row is read twice (the second time from the caches).
+__global__ void __launch_bounds__(256) i8_quant_kernel(const __nv_bfloat16 *__restrict__ x,
+                                                       int64_t M, int64_t K, int64_t ldx,
+                                                       uint8_t *__restrict__ q,
+                                                       float *__restrict__ scale,
+                                                       int *__restrict__ status) {
+  __shared__ uint32_t part[8];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t m = blockIdx.x;
+  const uint4 *src = reinterpret_cast<const uint4 *>(x + m * ldx);
+  const int64_t nv = K / 8;
+  uint32_t mx = 0, bad = 0;
+  for (int64_t i = threadIdx.x; i < nv; i += 256) {
+    const uint4 t = __ldg(src + i);
+    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+    mx = max(mx, bf16_amax_bits(w, bad));
+  }
+  mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = max(mx, part[i]);
+  const float amax = fmaxf(__uint_as_float(mx << 16), 0x1p-64f);
+  const float c = __fdiv_rn(127.0f, amax);
+  if (threadIdx.x == 0) {
+    scale[m] = __fdiv_rn(amax, 127.0f);
+    if (mx >= 0x7F80u && status) atomicOr(status, 1);
+  }
+  uint2 *dst = reinterpret_cast<uint2 *>(q + m * K);
+  for (int64_t i = threadIdx.x; i < nv; i += 256) {
+    const uint4 t = __ldg(src + i);
+    dst[i] = make_uint2(i8_codes4(t.x, t.y, c), i8_codes4(t.z, t.w, c));
+  }
+}
+
+}  // namespace bq

@@ -494,6 +494,112 @@ int bq_gemm_mxfp8_mxfp4_epilogue_noalloc(const void *a_q, const void *a_sf, cons
 /* Size in bytes of the library-owned scratch array used by the _noalloc call. */
 size_t bq_noalloc_scratch_bytes(void);
 
+/* ---- int8 products --------------------------------------------------------
+ *
+ * No counterpart on the pages: the integer form of the linear layer above, for
+ * checkpoints quantized to 8-bit integers with one scale for each token and
+ * each output channel. */
+
+/* bq_act_quant_int8 -- per-row int8 quantization of bf16 (a token's activations,
+ * or a weight's output channels):
+ *   amax = max(max_k |x[m, k]|, 2^-64);  scale[m] = fp32(amax / 127)
+ *   q[m, k] = the integer nearest 127 x[m, k] / amax, ties to even
+ * exactly, for finite input; q stands for q * scale[m].
+ *   x_bf16  [M, K] bf16, row stride ldx elements (ldx >= K, ldx % 8 == 0, base
+ *           16-byte aligned); K > 0 and K % 16 == 0
+ *   q_s8    out [M, K] signed 8-bit codes (-127 .. 127), row stride K, 16-byte aligned
+ *   scale   out [M] fp32, 4-byte aligned
+ *   d_status as bq_act_quant (a row with a NaN or Inf is unspecified).
+ * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_ARCH, BQ_ERR_CUDA. */
+int bq_act_quant_int8(const void *x_bf16, int64_t M, int64_t K, int64_t ldx, void *q_s8,
+                      float *scale, int *d_status, bq_stream_t stream);
+
+/* bq_gemm_int8_int8 -- y = bf16(a_scale[m] b_scale[n] sum_k a[m,k] b[n,k]) with
+ * signed 8-bit operands on tcgen05.mma kind::i8.  The sums are exact 32-bit
+ * integers (any codes, -128 included: K <= 131056 keeps them in range), scaled
+ * in fp32 and rounded to bf16 once.
+ *   a_s8 [M, K], b_s8 [N, K] dense, 16-byte aligned; K % 16 == 0, N % 8 == 0
+ *   a_scale [M], b_scale [N] fp32, 4-byte aligned
+ *   y_bf16 [M, N] out, 16-byte aligned
+ * The _epilogue form: y = bf16(act(alpha a_scale b_scale sum + bias) + residual)
+ * with bq_epilogue's options except the quantized output (BQ_ERR_INVALID), and
+ * bq_batch (its scale strides step the fp32 scales: bytes, multiples of 4).  It
+ * needs no workspace.  Stream order as the GEMMs above: b may be read early
+ * (a_scale, b_scale, bias and residual are not).
+ * Schedules (bq_gemm_config): swap_ab 1: block_n 32, 64 or 128 activation rows
+ * per tile, split_k 1 .. 8 CTAs of a cluster (split_mode AUTO or CLUSTER).
+ * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_INVALID, BQ_ERR_ARCH,
+ * BQ_ERR_CUDA. */
+int bq_gemm_int8_int8(const void *a_s8, const float *a_scale, const void *b_s8,
+                      const float *b_scale, int64_t M, int64_t N, int64_t K, void *y_bf16,
+                      bq_stream_t stream);
+int bq_gemm_int8_int8_epilogue(const void *a_s8, const float *a_scale, const void *b_s8,
+                               const float *b_scale, int64_t M, int64_t N, int64_t K, void *y_bf16,
+                               const bq_epilogue *epi, const bq_batch *batch,
+                               const bq_gemm_config *cfg, bq_stream_t stream);
+
+/* ---- gated feed-forward block ---------------------------------------------
+ *
+ * No counterpart on the pages: the gated form of their MLP's up-projection. */
+
+enum { BQ_GATE_SILU = 0, BQ_GATE_GELU = 1 };
+
+/* act: BQ_GATE_SILU (g / (1 + e^-g)) or BQ_GATE_GELU (the erf form).
+ * gu_out: optional out [M, 2 N] bf16, 16-byte aligned: g in columns 0 .. N - 1 and
+ * u in N .. 2 N - 1, each rounded to bf16 (h is formed from g and u before that
+ * rounding); the backward pass reads it.  q_out / sf_out: the quantized h, as
+ * bq_epilogue's (bq_act_quant of the bf16 h; N % 32 == 0; h_bf16 may then be NULL). */
+typedef struct {
+  float alpha;
+  int act;
+  void *gu_out;
+  void *q_out;
+  void *sf_out;
+} bq_gated_epilogue;
+
+/* bq_gemm_gated -- h = bf16(act(g) u), g = alpha A Wg^T, u = alpha A Wu^T: both
+ * projections, the activation, the product and the optional quantization for
+ * the down projection in one kernel.
+ *   weight_kind 0 mxfp4, 1 fp8blk32, 2 mxfp8: A, its scales, and each weight with
+ *               its scales as in the GEMM of that kind (K % 32 == 0; mxfp4 128)
+ *   weight_kind 6 int8: operands and fp32 scales as in bq_gemm_int8_int8
+ *   b_gate, b_up [N, K] weights; h_bf16 [M, N] out, N % 8 == 0, 16-byte aligned
+ *   epi NULL: alpha 1, SiLU, no further outputs.
+ * Schedules as bq_gemm_int8_int8, but MX tiles of 32 or 64 rows hold all M rows
+ * (else BQ_ERR_INVALID).  Stream order as the GEMMs above: both weights
+ * (and MX weight scales) may be read early.  A NaN or Inf in a quantized h is
+ * reported by bq_device_status.
+ * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_INVALID (kind, act,
+ * schedule), BQ_ERR_ARCH, BQ_ERR_CUDA. */
+int bq_gemm_gated(int weight_kind, const void *a_q, const void *a_sf, const void *b_gate,
+                  const void *gate_sf, const void *b_up, const void *up_sf, int64_t M, int64_t N,
+                  int64_t K, void *h_bf16, const bq_gated_epilogue *epi,
+                  const bq_gemm_config *cfg, bq_stream_t stream);
+
+/* The schedule that bq_gemm_int8_int8_epilogue (gated 0, weight_kind 6) or
+ * bq_gemm_gated (gated 1) picks, as bq_gemm_plan reports it.  Host-only. */
+int bq_ffn_plan(int weight_kind, int gated, int64_t M, int64_t N, int64_t K, int64_t batch,
+                const bq_gemm_config *cfg, int num_sms, bq_gemm_config *out);
+
+/* bq_gated_grad_quant -- backward pass of h = act(g) u, quantized for the two
+ * products that follow:
+ *   d = [dG | dU] [M, 2 N],  dG = dH u act'(g),  dU = dH act(g),
+ * each value rounded to bf16 and then quantized exactly as bq_grad_quant_dual
+ * quantizes a [M, 2 N] gradient (rounding, seed, q_row, sf_row, q_t, sf_t as
+ * there).  With Wg and Wu stacked to W [2 N, K] the gradients are
+ *   dX = bq_gemm_e5m2_mxfp8(q_row, bq_quant_transposed(W), M, K, 2 N)
+ *   dW = bq_gemm_e5m2_mxfp8(q_t, bq_quant_transposed(X), 2 N, K, M).
+ *   dh_bf16 [M, N] (row stride ld_dh >= N), gu_bf16 [M, 2 N] as bq_gemm_gated
+ *   keeps it (row stride ld_gu >= 2 N); M % 32 == 0, N % 32 == 0, strides % 8 == 0,
+ *   bases 16-byte aligned
+ *   d_bf16  optional out [M, 2 N] bf16, 16-byte aligned: d itself
+ *   d_status as bq_act_quant, of d.
+ * Errors: as bq_grad_quant_dual, BQ_ERR_INVALID for a bad act. */
+int bq_gated_grad_quant(const void *dh_bf16, int64_t ld_dh, const void *gu_bf16, int64_t ld_gu,
+                        int64_t M, int64_t N, int act, int rounding, uint64_t seed, void *q_row,
+                        void *sf_row, void *q_t, void *sf_t, void *d_bf16, int *d_status,
+                        bq_stream_t stream);
+
 /* ---- diagnostics -------------------------------------------------------- */
 
 /* Reads and clears the library's device error word on the current device.

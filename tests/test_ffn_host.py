@@ -1,0 +1,127 @@
+"""Host-side checks of the int8 and gated entry points: what they refuse (nothing is
+launched; no device is needed) and the schedules they pick."""
+import ctypes
+
+import pytest
+import torch
+
+import block_scaled_precision_quant_b200 as bq
+from block_scaled_precision_quant_b200 import build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def L():
+    build.build()
+    return bq.lib()
+
+
+P = 1 << 20  # stands for an aligned address; the checks come before any use of it
+
+
+def test_quant_refusals(L):
+    def call(x=P, M=4, K=32, ldx=32, q=P, s=P):
+        return L.bq_act_quant_int8(x, M, K, ldx, q, s, None, None)
+    assert call(x=None) == call(q=None) == call(s=None) == bq.BQ_ERR_NULL
+    assert call(K=24) == call(K=0) == call(M=-1) == call(ldx=24) == bq.BQ_ERR_SHAPE
+    assert call(x=P + 2) == call(ldx=36) == call(q=P + 8) == call(s=P + 2) == bq.BQ_ERR_ALIGN
+
+
+def product(L, a=P, sa=P, b=P, sb=P, M=4, N=8, K=32, y=P, epi=None, batch=None, cfg=None):
+    ref = lambda s: None if s is None else ctypes.byref(s)  # noqa: E731
+    return L.bq_gemm_int8_int8_epilogue(a, sa, b, sb, M, N, K, y, ref(epi), ref(batch), ref(cfg),
+                                        None)
+
+
+def test_product_refusals(L):
+    for k in ("a", "sa", "b", "sb", "y"):
+        assert product(L, **{k: None}) == bq.BQ_ERR_NULL
+        assert product(L, **{k: P + 2}) == bq.BQ_ERR_ALIGN
+    for kw in (dict(K=24), dict(K=0), dict(N=12), dict(M=-1), dict(K=131072), dict(N=1 << 32)):
+        assert product(L, **kw) == bq.BQ_ERR_SHAPE
+    E = bq.Epilogue
+    assert product(L, epi=E(None, None, 0, 1.0, 2, None, None)) == bq.BQ_ERR_INVALID
+    assert product(L, epi=E(None, None, 0, 1.0, 0, P, P)) == bq.BQ_ERR_INVALID
+    assert product(L, epi=E(P + 2, None, 0, 1.0, 0, None, None)) == bq.BQ_ERR_ALIGN
+    assert product(L, epi=E(None, P, 4, 1.0, 0, None, None)) == bq.BQ_ERR_ALIGN
+    B = bq.Batch
+    assert product(L, batch=B(2, 128, 16, 0, 0, 0, 0)) == bq.BQ_ERR_SHAPE  # outputs on top
+    assert product(L, batch=B(2, 128, 2, 0, 0, 64, 0)) == bq.BQ_ERR_ALIGN
+    assert product(L, batch=B(-1, 0, 0, 0, 0, 0, 0)) == bq.BQ_ERR_SHAPE
+    for c in (dict(block_n=48), dict(split_k=9), dict(split_mode=bq.BQ_SPLIT_WORKSPACE),
+              dict(k_chunks=2), dict(split_k=-1), dict(swap_ab=2), dict(cta_pair=3)):
+        assert product(L, cfg=bq.config(**c)) == bq.BQ_ERR_INVALID
+
+
+def gated(L, kind=2, a=P, sa=P, g=P, sg=P, u=P, su=P, M=4, N=32, K=128, h=P, epi=None, cfg=None):
+    ref = lambda s: None if s is None else ctypes.byref(s)  # noqa: E731
+    return L.bq_gemm_gated(kind, a, sa, g, sg, u, su, M, N, K, h, ref(epi), ref(cfg), None)
+
+
+def test_gated_refusals(L):
+    for kind in (3, 4, 5, 7, -1):
+        assert gated(L, kind=kind) == bq.BQ_ERR_INVALID
+    for kind in (0, 1, 2, 6):
+        for k in ("a", "sa", "g", "sg", "u", "su", "h"):
+            assert gated(L, kind=kind, **{k: None}) == bq.BQ_ERR_NULL
+            assert gated(L, kind=kind, **{k: P + 2}) == bq.BQ_ERR_ALIGN
+    assert gated(L, kind=0, g=P + 16) == bq.BQ_ERR_ALIGN  # packed codes: 32 bytes
+    assert gated(L, kind=0, K=96) == gated(L, K=48) == gated(L, N=36) == bq.BQ_ERR_SHAPE
+    assert gated(L, kind=6, K=131072) == bq.BQ_ERR_SHAPE
+    E = bq.GatedEpilogue
+    assert gated(L, epi=E(1.0, 2, None, None, None)) == bq.BQ_ERR_INVALID
+    assert gated(L, epi=E(1.0, 0, None, P, None)) == bq.BQ_ERR_NULL
+    assert gated(L, N=40, epi=E(1.0, 0, None, P, P)) == bq.BQ_ERR_SHAPE
+    assert gated(L, epi=E(1.0, 0, P + 2, None, None)) == bq.BQ_ERR_ALIGN
+    assert gated(L, epi=E(1.0, 0, None, P + 8, P)) == bq.BQ_ERR_ALIGN
+    assert gated(L, cfg=bq.config(block_n=16)) == bq.BQ_ERR_INVALID
+
+
+def test_grad_refusals(L):
+    def call(dh=P, ld=64, gu=P, ldg=128, M=32, N=64, act=0, rnd=0, q=P, sf=P, qt=P, st=P, d=None):
+        return L.bq_gated_grad_quant(dh, ld, gu, ldg, M, N, act, rnd, 0, q, sf, qt, st, d, None,
+                                     None)
+    for k in ("dh", "gu", "q", "sf", "qt", "st"):
+        assert call(**{k: None}) == bq.BQ_ERR_NULL
+    for k in ("dh", "gu", "q", "qt", "d"):
+        assert call(**{k: P + 2}) == bq.BQ_ERR_ALIGN
+    assert call(act=2) == call(rnd=2) == bq.BQ_ERR_INVALID
+    assert call(M=33) == call(N=48) == call(N=0) == call(M=-32) == bq.BQ_ERR_SHAPE
+    assert call(ld=32) == call(ldg=120) == bq.BQ_ERR_SHAPE
+    assert call(ld=68) == call(ldg=132) == bq.BQ_ERR_ALIGN
+
+
+def test_binding_refusals():
+    i8 = torch.zeros((4, 32), dtype=torch.int8)
+    f = torch.zeros(32)
+    with pytest.raises(ValueError):
+        bq.act_quant_int8(torch.zeros((4, 32), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        bq.gemm_int8_int8(i8, f, i8, f, 4, 4, 32)
+    with pytest.raises(ValueError):
+        bq.gemm(bq.W_INT8, i8, f, i8, f, 4, 4, 32, quantize_out=True)
+    with pytest.raises(ValueError):
+        bq.gemm_gated(bq.W_INT8, i8, f, i8, f, i8, f, 4, 4, 32)
+    with pytest.raises(ValueError):
+        bq.gated_grad_quant(torch.zeros((32, 32), dtype=torch.bfloat16),
+                            torch.zeros((32, 64), dtype=torch.bfloat16))
+
+
+def test_plans():
+    c = bq.ffn_plan(41, 4608, 1536)
+    assert c.swap_ab == 1 and c.block_n == 64 and 36 * c.split_k <= 148 and c.split_k > 1
+    c = bq.ffn_plan(1, 16384, 8192, weight_kind=bq.W_FP8BLK32, gated=True)
+    assert c.swap_ab == 1 and c.block_n == 32 and c.split_k == 1
+    # an MX tile shorter than a scale atom holds all rows
+    for M, bn, ok in ((32, 32, True), (33, 32, False), (64, 64, True), (65, 64, False),
+                      (300, 128, True)):
+        for kind in (bq.W_MXFP4, bq.W_FP8BLK32, bq.W_MXFP8, bq.W_INT8):
+            kw = dict(config=bq.config(block_n=bn, swap_ab=1), weight_kind=kind, gated=True)
+            if ok or kind == bq.W_INT8:
+                assert bq.ffn_plan(M, 256, 256, **kw).block_n == bn
+            else:
+                with pytest.raises(bq.BqError) as e:
+                    bq.ffn_plan(M, 256, 256, **kw)
+                assert e.value.status == bq.BQ_ERR_INVALID
+    for kind, gate in ((bq.W_MXFP8, False), (bq.W_A4W4, True), (bq.W_NVFP4, True)):
+        with pytest.raises(bq.BqError):
+            bq.ffn_plan(41, 4608, 1536, weight_kind=kind, gated=gate)

@@ -1,0 +1,246 @@
+"""The int8 row quantizer (bit-exact) and the int8 product against 64-bit forms."""
+import pytest
+import torch
+
+import block_scaled_precision_quant_b200 as bq
+import ffn_ref
+from ffn_ref import Operand, close, gelu, int8_rows, int8_tol
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(M, K, seed, ld=None):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((M, ld or K), generator=g)
+    x = x * 2.0 ** torch.randint(-12, 13, (M, 1), generator=g).float()
+    return x.to(torch.bfloat16).cuda()
+
+
+def check_quant(x, q, s):
+    rq, rs = int8_rows(x)
+    assert torch.equal(q, rq)
+    # the scale is one correctly rounded quotient
+    assert torch.equal(s, rs.float())
+
+
+# one row, rows shorter and longer than a block's registers, odd tails of every kind
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 4096), (3, 48), (7, 240), (41, 1536), (130, 2064),
+                                 (33, 8192), (5, 8208), (2, 16400), (3, 65552), (1, 131056),
+                                 (2500, 272)])
+def test_quant_rows(M, K):
+    x = rows(M, K, M + K)
+    q, s = bq.act_quant_int8(x)
+    check_quant(x, q, s)
+
+
+def test_quant_ties_go_to_even():
+    """Every pair of 8-bit significands and the binades a code can span: ties among
+    them are decided exactly."""
+    big = torch.arange(128, 256).float()
+    x = torch.zeros((128, 9 * 256))
+    for t in range(9):
+        x[:, 256 * t:256 * t + 256] = torch.arange(256).float() * 2.0 ** -t
+    x = torch.where(x.abs() > big[:, None], torch.zeros(()), x)
+    x[:, 0] = big
+    x[::2] *= -1
+    x = x.to(torch.bfloat16).cuda()
+    q, s = bq.act_quant_int8(x)
+    check_quant(x, q, s)
+    n = x.double() * 127 / x.double().abs().amax(1, keepdim=True)
+    assert int(((n - n.floor()) == 0.5).sum()) == 444  # of these inputs, counted in 64 bits
+
+
+def test_quant_small_zero_and_large_rows():
+    x = torch.zeros((6, 64))
+    x[1] = 2.0 ** -64
+    x[2, 3] = 2.0 ** -126
+    x[3] = torch.linspace(-3, 3, 64) * 1e38  # (the span itself would overflow to an Inf)
+    x[4, 0], x[4, 1] = 1e-20, -3e-20
+    x[5] = 2.0 ** -133
+    x = x.to(torch.bfloat16).cuda()
+    q, s = bq.act_quant_int8(x)
+    check_quant(x, q, s)
+    assert int(q[0].abs().max()) == 0 and int(q[1].min()) == 127
+
+
+def test_quant_row_stride_outputs_and_status():
+    wide = rows(45, 200, 3)
+    x = wide[:, :160]
+    q = torch.full((46, 160), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((46,), 5.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bq.act_quant_int8(x, q=q[:45], scale=s[:45], status=st)
+    check_quant(x, q[:45], s[:45])
+    assert bool((q[45] == 77).all()) and float(s[45]) == 5.0 and int(st) == 0
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        y = x.clone()
+        y[44, 159] = bad
+        st.zero_()
+        q2, s2 = bq.act_quant_int8(y, status=st)
+        assert int(st) == 1
+        check_quant(y[:44], q2[:44], s2[:44])  # the other rows stand
+
+
+def product(M, N, K, seed, bias=False, res=False, act=0, alpha=1.0, config=None, ldres=None):
+    a, b = Operand("int8", M, K, seed), Operand("int8", N, K, seed + 1)
+    g = torch.Generator().manual_seed(seed + 2)
+    bv = torch.randn((N,), generator=g).to(torch.bfloat16).cuda() if bias else None
+    rv = (torch.randn((M, ldres or N), generator=g) * 3).to(torch.bfloat16).cuda() if res else None
+    if res:
+        rv = rv[:, :N]
+    y = bq.gemm(bq.W_INT8, a.q, a.sf, b.q, b.sf, M, N, K, bias=bv, residual=rv, act=act,
+                alpha=alpha, config=config)
+    bq.device_status()
+    p = alpha * ffn_ref.product(a, b)
+    zero = torch.zeros((), dtype=torch.float64, device="cuda")
+    bd, rd = (bv.double() if bias else zero), (rv.double() if res else zero)
+    pre = p + bd
+    ref = (gelu(pre) if act else pre) + rd
+    close(y, ref, int8_tol(p, bd, pre, rd, ref, act), f"{M}x{N}x{K}")
+    return y
+
+
+# from one row to many, sizes that end inside tiles of every kind
+@pytest.mark.parametrize("M,N,K", [
+    (1, 8, 16), (1, 4608, 1536), (2, 136, 144), (8, 1536, 6144), (31, 128, 128), (32, 264, 2064),
+    (33, 512, 496), (41, 4608, 1536), (64, 1000, 1040), (65, 128, 272), (127, 2048, 512),
+    (128, 520, 4096), (129, 264, 80), (200, 1032, 1008), (257, 640, 912), (384, 256, 2048),
+    (500, 776, 656), (1003, 520, 400)])
+def test_product(M, N, K):
+    product(M, N, K, M * 7 + N + K)
+
+
+@pytest.mark.parametrize("M", [1, 41, 100, 300])
+@pytest.mark.parametrize("bias,res,act,alpha", [(True, False, 0, 1.0), (False, True, 0, 1.0),
+                                                (True, True, 1, 1.0), (False, False, 1, 0.25),
+                                                (True, True, 0, -2.0)])
+def test_epilogues(M, bias, res, act, alpha):
+    product(M, 456, 336, M, bias, res, act, alpha, ldres=472)
+
+
+@pytest.mark.parametrize("bn", [32, 64, 128])
+@pytest.mark.parametrize("split", [1, 2, 3, 5, 8])
+def test_swap_schedules(bn, split):
+    product(70, 392, 1168, bn + split, bias=True, config=bq.config(block_n=bn, split_k=split,
+                                                                   swap_ab=1))
+
+
+def test_sums_are_exact_at_their_largest():
+    """The longest K with every code at its end of the range: |sum| = K 2^14 just
+    below 2^31; with unit scales the output is that sum rounded to bf16."""
+    K = 131056
+    a = torch.full((2, K), -128, dtype=torch.int8, device="cuda")
+    b = torch.full((8, K), -128, dtype=torch.int8, device="cuda")
+    b[1] = 127
+    one = torch.ones(8, device="cuda")
+    for cfg in (None, bq.config(split_k=1), bq.config(split_k=8)):
+        y = bq.gemm_int8_int8(a, one[:2].contiguous(), b, one, 2, 8, K, config=cfg)
+        bq.device_status()
+        ref = (a.double() @ b.double().t()).to(torch.bfloat16)
+        assert torch.equal(y, ref)
+
+
+def test_split_does_not_change_a_bit():
+    a, b = Operand("int8", 41, 4096, 5), Operand("int8", 512, 4096, 6)
+    ys = [bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, 41, 512, 4096,
+                            config=bq.config(split_k=s, block_n=n))
+          for s in (1, 2, 7, 8) for n in (32, 64, 128)]
+    bq.device_status()
+    assert all(torch.equal(ys[0], y) for y in ys[1:])
+
+
+@pytest.mark.parametrize("M", [20, 64, 300])
+def test_batch_with_broadcast_operands(M):
+    count, N, K = 3, 200, 272
+    a = [Operand("int8", M, K, 10 + i) for i in range(count)]
+    b = [Operand("int8", N, K, 20 + i) for i in range(count)]
+    res = torch.randn((count, M, N), device="cuda").to(torch.bfloat16)
+    aq = torch.stack([t.q for t in a])
+    asf = torch.stack([t.sf for t in a])
+    bq_, bsf = torch.stack([t.q for t in b]), torch.stack([t.sf for t in b])
+    for shared in ("", "a", "b"):
+        sa, sb = (0 if shared == "a" else 1), (0 if shared == "b" else 1)
+        y = bq.gemm_int8_int8(aq, asf, bq_, bsf, M, N, K, residual=res, batch=dict(
+            count=count, stride_a=sa * M * K, stride_a_sf=sa * 4 * M, stride_b=sb * N * K,
+            stride_b_sf=sb * 4 * N, stride_y=2 * M * N, stride_res=2 * M * N))
+        bq.device_status()
+        for i in range(count):
+            p = ffn_ref.product(a[i * sa], b[i * sb])
+            r = res[i].double()
+            z = torch.zeros_like(p)
+            close(y[i], p + r, int8_tol(p, z, p, r, p + r, 0), f"{shared} {i}")
+
+
+def test_rows_behind_the_last_stay_as_they_were():
+    M, N, K = 37, 136, 160
+    a, b = Operand("int8", M, K, 1), Operand("int8", N, K, 2)
+    y = torch.full((M + 3, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, M, N, K, y=y[:M])
+    bq.device_status()
+    assert bool((y[M:] == 9).all())
+
+
+def test_linear_layer_chain_captured_and_replayed():
+    """Quantizer and product back to back, captured once and replayed on new inputs,
+    the weights quantized by the same quantizer."""
+    M, N, K = 41, 1536, 512
+    w = rows(N, K, 9)
+    wq, ws = bq.act_quant_int8(w)
+    x = rows(M, K, 1)
+    q = torch.empty((M, K), dtype=torch.int8, device="cuda")
+    s = torch.empty((M,), device="cuda")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        bq.act_quant_int8(x, q=q, scale=s)
+        bq.gemm_int8_int8(q, s, wq, ws, M, N, K, y=y)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (2, 3, 4):
+        x.copy_(rows(M, K, seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        rq, rs = int8_rows(x)
+        p = (rq.double() @ wq.double().t()) * rs.float().double()[:, None] * ws.double()
+        z = torch.zeros_like(p)
+        close(got, p, int8_tol(p, z, p, z, p, 0), f"replay {seed}")
+    bq.device_status()
+
+
+def test_two_streams_at_once():
+    ops = [(Operand("int8", 64, 2048, s), Operand("int8", 1024, 2048, s + 50)) for s in range(2)]
+    one = [bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, 64, 1024, 2048) for a, b in ops]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ops]
+    outs = [[], []]
+    for _ in range(20):
+        for i, (st, (a, b)) in enumerate(zip(streams, ops)):
+            with torch.cuda.stream(st):
+                outs[i].append(bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, 64, 1024, 2048))
+    torch.cuda.synchronize()
+    bq.device_status()
+    for i in range(2):
+        assert all(torch.equal(one[i], y) for y in outs[i])
+
+
+def test_empty_calls():
+    a, b = Operand("int8", 4, 32, 1), Operand("int8", 8, 32, 2)
+    assert bq.gemm_int8_int8(a.q[:0], a.sf[:0], b.q, b.sf, 0, 8, 32).shape == (0, 8)
+    q, s = bq.act_quant_int8(torch.empty((0, 32), dtype=torch.bfloat16, device="cuda"))
+    assert q.shape == (0, 32) and s.shape == (0,)
+
+
+def test_arch_override_refuses():
+    a, b = Operand("int8", 4, 32, 1), Operand("int8", 8, 32, 2)
+    bq.lib().bq_debug_override_compute_capability(9, 0)
+    try:
+        with pytest.raises(bq.BqError) as e:
+            bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, 4, 8, 32)
+        assert e.value.status == bq.BQ_ERR_ARCH
+    finally:
+        bq.lib().bq_debug_override_compute_capability(-1, -1)
