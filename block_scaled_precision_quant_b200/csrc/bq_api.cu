@@ -243,6 +243,9 @@ int make_plan(int64_t M, int64_t N, int64_t K, int64_t batch, const bq_gemm_conf
     if (M > 64) return BQ_ERR_INVALID;
     p->bn = req_bn ? req_bn : (M <= 32 ? 32 : 64);
     if (p->bn != 32 && p->bn != 64) return BQ_ERR_INVALID;
+    // A second 32-row tile would begin in the middle of a scale atom and name its
+    // scales by an odd TMEM column, which the block-scaled MMA does not take.
+    if (p->bn < M) return BQ_ERR_INVALID;
     p->tiles_p = ceil_div(N, 128);
     p->tiles_q = ceil_div(M, p->bn);
   } else {

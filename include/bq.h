@@ -345,7 +345,7 @@ typedef struct {
 
 /* Optional schedule override (tests and sweeps); NULL = built-in dispatch.
  * block_n:    0 (auto); 128 or 256 weight rows per CTA tile, or with swap_ab 32
- *             or 64 activation rows per CTA tile.
+ *             or 64 activation rows per CTA tile (32 only for M <= 32).
  * split_k:    0 (auto) or 1..16 slices of K.
  * swap_ab:    -1 (auto), 0, or 1 (weights on the 128-row MMA side, for M <= 64).
  * split_mode: how K slices are combined, always in slice order:

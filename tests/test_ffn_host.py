@@ -125,3 +125,15 @@ def test_plans():
     for kind, gate in ((bq.W_MXFP8, False), (bq.W_A4W4, True), (bq.W_NVFP4, True)):
         with pytest.raises(bq.BqError):
             bq.ffn_plan(41, 4608, 1536, weight_kind=kind, gated=gate)
+
+
+def test_block_scaled_gemm_refuses_a_second_32_row_tile():
+    """32-row decode tiles hold all activation rows: a second one would begin in the
+    middle of a scale atom."""
+    for kind in (bq.W_MXFP4, bq.W_FP8BLK32, bq.W_MXFP8, bq.W_A4W4, bq.W_GRAD, bq.W_NVFP4):
+        assert bq.plan(32, 512, 1024, weight_kind=kind,
+                       config=bq.config(block_n=32, swap_ab=1)).block_n == 32
+        for M in (33, 64):
+            with pytest.raises(bq.BqError) as e:
+                bq.plan(M, 512, 1024, weight_kind=kind, config=bq.config(block_n=32, swap_ab=1))
+            assert e.value.status == bq.BQ_ERR_INVALID
