@@ -10,6 +10,7 @@
 #include "bq.h"
 #include "bq_host.cuh"
 #include "gated_grad.cuh"
+#include "lin_pair.cuh"
 #include "lin_swap.cuh"
 #include "quant_i8.cuh"
 
@@ -73,10 +74,47 @@ int operand_map(CUtensorMap* m, const void* base, bool fp4, int64_t K, int64_t r
   return r == CUDA_SUCCESS ? BQ_OK : BQ_ERR_ALIGN;
 }
 
+// An MX scale buffer as (128 words, K atoms, 128-row bands), boxes of one atom.
+int scale_map(CUtensorMap* m, const void* base, int64_t rows, int64_t K) {
+  auto encode = bqh::tensor_map_encoder();
+  if (!encode) return BQ_ERR_CUDA;
+  const int64_t katoms = ceil_div(K, 128), bands = ceil_div(rows, 128);
+  const cuuint64_t dims[3] = {128u, static_cast<cuuint64_t>(katoms),
+                              static_cast<cuuint64_t>(bands)};
+  const cuuint64_t strides[2] = {512u, static_cast<cuuint64_t>(katoms * 512)};
+  const cuuint32_t box[3] = {128u, 1u, 1u};
+  const cuuint32_t step[3] = {1u, 1u, 1u};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims,
+                            strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? BQ_OK : BQ_ERR_ALIGN;
+}
+
+// A bf16 output [batch][M][ld] of N columns: boxes of 32 columns x 128 rows with
+// the 64-byte swizzle of the epilogue's staging tile.
+int output_map(CUtensorMap* m, const void* y, int64_t M, int64_t N, int64_t ld, int64_t batch,
+               int64_t batch_bytes) {
+  auto encode = bqh::tensor_map_encoder();
+  if (!encode) return BQ_ERR_CUDA;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * ld),
+                                 static_cast<cuuint64_t>(batch > 1 ? batch_bytes : 2 * ld * M)};
+  const cuuint32_t box[3] = {32u, 128u, 1u};
+  const cuuint32_t step[3] = {1u, 1u, 1u};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(y), dims,
+                            strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? BQ_OK : BQ_ERR_ALIGN;
+}
+
 // ---------------------------------------------------------------- schedule --
 
 struct Plan {
-  int bn = 0;      // activation rows of a tile
+  bool pair = false;  // 256-row tiles on pairs of SMs (lin_pair.cuh), else lin_swap.cuh
+  int bn = 0;         // swap: activation rows of a tile; pair: weight rows (256)
   int splits = 1;  // K slices (CTAs of a cluster)
   int64_t tiles_p = 0, tiles_q = 0, tiles = 0;
   int kt = 0;
@@ -87,21 +125,37 @@ constexpr int kMaxSplit = 8;  // portable cluster size
 int check_config(const bq_gemm_config* cfg) {
   if (!cfg) return BQ_OK;
   const bq_gemm_config& c = *cfg;
-  if (c.block_n != 0 && c.block_n != 32 && c.block_n != 64 && c.block_n != 128)
+  if (c.block_n != 0 && c.block_n != 32 && c.block_n != 64 && c.block_n != 128 &&
+      c.block_n != 256)
     return BQ_ERR_INVALID;
-  if (c.split_k < 0 || c.split_k > kMaxSplit || c.swap_ab < -1 || c.swap_ab == 0 ||
+  if (c.split_k < 0 || c.split_k > kMaxSplit || c.swap_ab < -1 ||
       c.swap_ab > 1 || (c.split_mode != BQ_SPLIT_AUTO && c.split_mode != BQ_SPLIT_CLUSTER) ||
-      c.k_chunks < 0 || c.k_chunks > 1 || c.cta_pair < 0 || c.cta_pair > 1)
+      c.k_chunks < 0 || c.k_chunks > 1 || c.cta_pair < 0 || c.cta_pair > 2)
     return BQ_ERR_INVALID;
+  // pairs: 256-row tiles, no split; everything else: tiles of one SM
+  const bool pair = c.swap_ab == 0 || c.cta_pair == 2 || c.block_n == 256;
+  const bool swap = c.swap_ab == 1 || c.cta_pair == 1 || c.split_k > 1 ||
+                    (c.block_n != 0 && c.block_n != 256);
+  if (pair && swap) return BQ_ERR_INVALID;
   return BQ_OK;
 }
 
-int make_plan(Kind kind, int64_t M, int64_t N, int64_t K, int64_t batch,
+int make_plan(Kind kind, bool gated, int64_t M, int64_t N, int64_t K, int64_t batch,
               const bq_gemm_config* cfg, int num_sms, Plan* p) {
   const bq_gemm_config c = cfg ? *cfg : bq_gemm_config{0, 0, -1, BQ_SPLIT_AUTO, 0, 0};
   // MX tiles start at the first row of a scale atom (lin_swap.cuh)
   if (kind != kInt8 && c.block_n != 0 && c.block_n < 128 && M > c.block_n) return BQ_ERR_INVALID;
   p->kt = static_cast<int>(ceil_div(K, 128));
+  const bool swap_asked = c.swap_ab == 1 || c.cta_pair == 1 || c.split_k > 0 || c.block_n == 32 ||
+                          c.block_n == 64 || c.block_n == 128;
+  p->pair = c.swap_ab == 0 || c.cta_pair == 2 || c.block_n == 256 || (!swap_asked && M > 128);
+  if (p->pair) {
+    p->bn = 256;
+    p->tiles_p = ceil_div(M, 256);
+    p->tiles_q = ceil_div(N, gated ? 128 : 256);
+    p->tiles = p->tiles_p * p->tiles_q * batch;
+    return p->tiles > 0x7FFFFFFF ? BQ_ERR_SHAPE : BQ_OK;
+  }
   p->bn = c.block_n ? c.block_n : (M <= 32 ? 32 : M <= 64 ? 64 : 128);
   p->tiles_p = ceil_div(N, 128);
   p->tiles_q = ceil_div(M, p->bn);
@@ -132,6 +186,26 @@ int launch_swap(const Plan& pl, const CUtensorMap& w0, const CUtensorMap& w1,
   }
   return launch(kern, dim3(static_cast<unsigned>(pl.tiles * pl.splits)), bq::kSwapThreads,
                 L::kBytes, pl.splits, stream, w0, w1, ta, a);
+}
+
+using Map = CUtensorMap;
+
+template <bool I8, bool GATED>
+int launch_pair(const Plan& pl, const Map& ta, const Map& w0, const Map& w1, const Map& sfa,
+                const Map& sf0, const Map& sf1, const Map& ty, const Map& tg, const Map& tu,
+                const bq::FfnArgs& a, const Device& dev, bq_stream_t stream) {
+  using L = bq::LinPairSmem<I8>;
+  auto kern = bq::lin_pair_kernel<I8, GATED>;
+  static bool ready[bqh::kMaxDevices] = {};
+  if (!ready[dev.index]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
+        cudaSuccess)
+      return BQ_ERR_CUDA;
+    ready[dev.index] = true;
+  }
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(dev.num_sms / 2, pl.tiles));
+  return launch(kern, dim3(static_cast<unsigned>(2 * pairs)), bq::kLinPairThreads, L::kBytes, 2,
+                stream, ta, w0, w1, sfa, sf0, sf1, ty, tg, tu, a);
 }
 
 template <bool I8, bool GATED>
@@ -173,7 +247,7 @@ int check_pointers(const Call& c, bool gated) {
     if (!c.w[w] || !c.w_sf[w]) return BQ_ERR_NULL;
   if (!aligned(c.a, 16) || !aligned(c.a_sf, i8 ? 4 : 16)) return BQ_ERR_ALIGN;
   for (int w = 0; w < (gated ? 2 : 1); ++w)
-    if (!aligned(c.w[w], c.kind == kMxfp4 ? 32 : 16) || !aligned(c.w_sf[w], i8 ? 4 : 16))
+    if (!aligned(c.w[w], c.kind == kMxfp4 ? 32 : 16) || !aligned(c.w_sf[w], 16))
       return BQ_ERR_ALIGN;
   return BQ_OK;
 }
@@ -218,7 +292,7 @@ int run(const Call& c, bool gated, bool empty, const bq_gemm_config* cfg, bq::Ff
   st = bqh::current_device(&dev);
   if (st != BQ_OK || empty) return st;
   Plan pl;
-  st = make_plan(c.kind, c.M, c.N, c.K, c.batch.count, cfg, dev.num_sms, &pl);
+  st = make_plan(c.kind, gated, c.M, c.N, c.K, c.batch.count, cfg, dev.num_sms, &pl);
   if (st != BQ_OK) return st;
   const bool i8 = c.kind == kInt8, fp4 = c.kind == kMxfp4;
   operand_args(c, g);
@@ -227,11 +301,39 @@ int run(const Call& c, bool gated, bool empty, const bq_gemm_config* cfg, bq::Ff
   g->splits = pl.splits;
   g->tiles_p = static_cast<int>(pl.tiles_p);
   g->tiles_q = static_cast<int>(pl.tiles_q);
+  CUtensorMap ta, tw[2];
+  if (pl.pair) {
+    g->raster_group = 4;
+    g->splits = 1;
+    st = operand_map(&ta, c.a, false, c.K, c.M, g->q_batched ? c.batch.count : 1,
+                     c.batch.stride_a, 128);
+    for (int w = 0; st == BQ_OK && w < (gated ? 2 : 1); ++w)
+      st = operand_map(&tw[w], c.w[w], fp4, c.K, c.N, g->p_batched ? c.batch.count : 1,
+                       c.batch.stride_b, 128);
+    if (st != BQ_OK) return st;
+    CUtensorMap sfa = ta, sf[2] = {ta, ta}, ty = ta, tg = ta, tu = ta;  // unused: placeholders
+    if (!i8) {
+      st = scale_map(&sfa, c.a_sf, c.M, c.K);
+      for (int w = 0; st == BQ_OK && w < 2; ++w) st = scale_map(&sf[w], c.w_sf[w], c.N, c.K);
+    }
+    if (st == BQ_OK && g->y)
+      st = output_map(&ty, g->y, c.M, c.N, c.N, c.batch.count, c.batch.stride_y);
+    if (st == BQ_OK && g->gu) st = output_map(&tg, g->gu, c.M, c.N, 2 * c.N, 1, 0);
+    if (st == BQ_OK && g->gu) st = output_map(&tu, g->gu + c.N, c.M, c.N, 2 * c.N, 1, 0);
+    if (st != BQ_OK) return st;
+    const bq_stream_t s = stream;
+    if (!gated)
+      return launch_pair<true, false>(pl, ta, tw[0], tw[0], sfa, sf[0], sf[1], ty, tg, tu, *g, dev,
+                                      s);
+    return i8 ? launch_pair<true, true>(pl, ta, tw[0], tw[1], sfa, sf[0], sf[1], ty, tg, tu, *g,
+                                        dev, s)
+              : launch_pair<false, true>(pl, ta, tw[0], tw[1], sfa, sf[0], sf[1], ty, tg, tu, *g,
+                                         dev, s);
+  }
   // One tile over all rows: its box ends at the last row (a box whose trailing
   // rows all lie outside the tensor copies slower).
   g->q_box_rows =
       pl.tiles_q == 1 ? static_cast<int>(std::min<int64_t>(pl.bn, (c.M + 7) / 8 * 8)) : pl.bn;
-  CUtensorMap ta, tw[2];
   st = operand_map(&ta, c.a, false, c.K, c.M, g->q_batched ? c.batch.count : 1, c.batch.stride_a,
                    g->q_box_rows);
   for (int w = 0; st == BQ_OK && w < (gated ? 2 : 1); ++w)
@@ -298,7 +400,7 @@ int bq_gemm_int8_int8_epilogue(const void* a_s8, const float* a_scale, const voi
     if (b.stride_a < 0 || b.stride_a_sf < 0 || b.stride_b < 0 || b.stride_b_sf < 0 ||
         b.stride_y <= 0 || b.stride_res < 0)
       return BQ_ERR_SHAPE;
-    if (b.stride_a % 16 || b.stride_b % 16 || b.stride_a_sf % 4 || b.stride_b_sf % 4 ||
+    if (b.stride_a % 16 || b.stride_b % 16 || b.stride_a_sf % 4 || b.stride_b_sf % 16 ||
         b.stride_y % 16 || b.stride_res % 16)
       return BQ_ERR_ALIGN;
   }
@@ -392,14 +494,14 @@ int bq_ffn_plan(int weight_kind, int gated, int64_t M, int64_t N, int64_t K, int
   int st = check_operands(c);
   if (st == BQ_OK) st = check_config(cfg);
   Plan pl;
-  if (st == BQ_OK) st = make_plan(c.kind, M, N, K, batch, cfg, num_sms, &pl);
+  if (st == BQ_OK) st = make_plan(c.kind, gated != 0, M, N, K, batch, cfg, num_sms, &pl);
   if (st != BQ_OK) return st;
   out->block_n = pl.bn;
   out->split_k = pl.splits;
-  out->swap_ab = 1;
+  out->swap_ab = pl.pair ? 0 : 1;
   out->split_mode = pl.splits > 1 ? BQ_SPLIT_CLUSTER : BQ_SPLIT_AUTO;
   out->k_chunks = 1;
-  out->cta_pair = 1;
+  out->cta_pair = pl.pair ? 2 : 1;
   return BQ_OK;
 }
 

@@ -519,15 +519,16 @@ int bq_act_quant_int8(const void *x_bf16, int64_t M, int64_t K, int64_t ldx, voi
  * integers (any codes, -128 included: K <= 131056 keeps them in range), scaled
  * in fp32 and rounded to bf16 once.
  *   a_s8 [M, K], b_s8 [N, K] dense, 16-byte aligned; K % 16 == 0, N % 8 == 0
- *   a_scale [M], b_scale [N] fp32, 4-byte aligned
+ *   a_scale [M] fp32, 4-byte aligned; b_scale [N] fp32, 16-byte aligned
  *   y_bf16 [M, N] out, 16-byte aligned
  * The _epilogue form: y = bf16(act(alpha a_scale b_scale sum + bias) + residual)
  * with bq_epilogue's options except the quantized output (BQ_ERR_INVALID), and
- * bq_batch (its scale strides step the fp32 scales: bytes, multiples of 4).  It
- * needs no workspace.  Stream order as the GEMMs above: b may be read early
+ * bq_batch (its scale strides step the fp32 scales: bytes, multiples of 4 for
+ * a_scale, of 16 for b_scale).  It needs no workspace.  Stream order as the GEMMs above: b may be read early
  * (a_scale, b_scale, bias and residual are not).
  * Schedules (bq_gemm_config): swap_ab 1: block_n 32, 64 or 128 activation rows
- * per tile, split_k 1 .. 8 CTAs of a cluster (split_mode AUTO or CLUSTER).
+ * per tile, split_k 1 .. 8 CTAs of a cluster (split_mode AUTO or CLUSTER);
+ * swap_ab 0: 256 x 256 tiles on pairs of SMs (cta_pair 2, block_n 256), unsplit.
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_INVALID, BQ_ERR_ARCH,
  * BQ_ERR_CUDA. */
 int bq_gemm_int8_int8(const void *a_s8, const float *a_scale, const void *b_s8,

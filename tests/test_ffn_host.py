@@ -36,6 +36,7 @@ def test_product_refusals(L):
     for k in ("a", "sa", "b", "sb", "y"):
         assert product(L, **{k: None}) == bq.BQ_ERR_NULL
         assert product(L, **{k: P + 2}) == bq.BQ_ERR_ALIGN
+    assert product(L, sb=P + 4) == bq.BQ_ERR_ALIGN
     for kw in (dict(K=24), dict(K=0), dict(N=12), dict(M=-1), dict(K=131072), dict(N=1 << 32)):
         assert product(L, **kw) == bq.BQ_ERR_SHAPE
     E = bq.Epilogue
@@ -48,7 +49,9 @@ def test_product_refusals(L):
     assert product(L, batch=B(2, 128, 2, 0, 0, 64, 0)) == bq.BQ_ERR_ALIGN
     assert product(L, batch=B(-1, 0, 0, 0, 0, 0, 0)) == bq.BQ_ERR_SHAPE
     for c in (dict(block_n=48), dict(split_k=9), dict(split_mode=bq.BQ_SPLIT_WORKSPACE),
-              dict(k_chunks=2), dict(split_k=-1), dict(swap_ab=2), dict(cta_pair=3)):
+              dict(k_chunks=2), dict(split_k=-1), dict(swap_ab=2), dict(cta_pair=3),
+              dict(swap_ab=0, split_k=2), dict(swap_ab=1, block_n=256),
+              dict(cta_pair=2, block_n=64), dict(cta_pair=1, swap_ab=0)):
         assert product(L, cfg=bq.config(**c)) == bq.BQ_ERR_INVALID
 
 

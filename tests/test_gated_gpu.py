@@ -74,6 +74,13 @@ def test_forward_swap_schedules(kind, bn, split):
 
 
 @pytest.mark.parametrize("kind", list(KIND))
+@pytest.mark.parametrize("M,N,K", [(1, 8, 128), (100, 136, 384), (128, 128, 1024),
+                                   (129, 264, 1152), (257, 1032, 256), (700, 520, 640)])
+def test_forward_pair_tiles(kind, M, N, K):
+    forward(kind, M, N, K, ACTS[(M + 1) % 2], M + N, keep=M != 128, config=bq.config(swap_ab=0))
+
+
+@pytest.mark.parametrize("kind", list(KIND))
 @pytest.mark.parametrize("M,N,K", [(1, 32, 128), (41, 1536, 512), (70, 160, 384), (130, 96, 256),
                                    (300, 416, 640)])
 @pytest.mark.parametrize("write_y", [True, False])

@@ -125,6 +125,21 @@ def test_swap_schedules(bn, split):
                                                                    swap_ab=1))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (100, 136, 400), (128, 256, 128), (129, 264, 1168),
+                                   (257, 520, 2064), (513, 1000, 640), (1300, 2056, 272)])
+@pytest.mark.parametrize("bias,res,act", [(False, False, 0), (True, True, 1)])
+def test_pair_tiles(M, N, K, bias, res, act):
+    product(M, N, K, M + K, bias, res, act, 0.5, bq.config(swap_ab=0), ldres=N + 8)
+
+
+def test_pair_tiles_equal_swap_tiles():
+    a, b = Operand("int8", 300, 1552, 5), Operand("int8", 776, 1552, 6)
+    ys = [bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, 300, 776, 1552, config=c)
+          for c in (bq.config(swap_ab=0), bq.config(swap_ab=1), bq.config(split_k=4))]
+    bq.device_status()
+    assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
 def test_sums_are_exact_at_their_largest():
     """The longest K with every code at its end of the range: |sum| = K 2^14 just
     below 2^31; with unit scales the output is that sum rounded to bf16."""
@@ -133,7 +148,7 @@ def test_sums_are_exact_at_their_largest():
     b = torch.full((8, K), -128, dtype=torch.int8, device="cuda")
     b[1] = 127
     one = torch.ones(8, device="cuda")
-    for cfg in (None, bq.config(split_k=1), bq.config(split_k=8)):
+    for cfg in (None, bq.config(split_k=1), bq.config(split_k=8), bq.config(swap_ab=0)):
         y = bq.gemm_int8_int8(a, one[:2].contiguous(), b, one, 2, 8, K, config=cfg)
         bq.device_status()
         ref = (a.double() @ b.double().t()).to(torch.bfloat16)
