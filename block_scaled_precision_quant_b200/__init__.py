@@ -193,13 +193,22 @@ def lib():
 
 # ------------------------------------------------------------------ helpers --
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream():
-    return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
+    torch = _torch()
+    if torch.cuda.is_initialized():  # the Stream object built below costs more than a launch
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def _ptr(t):
@@ -576,29 +585,33 @@ def gemm_e5m2_mxfp8(a_e5m2, a_sf, b_e4m3, b_sf, M, N, K, **kw):
 
 # -------------------------------------------- int8 and gated feed-forward ----
 
-def _device_index(torch, *ts):
-    """The calls run on the current device and stream: their tensors live there."""
-    here = torch.cuda.current_device() if torch.cuda.is_available() else -1
+def _here(torch, *ts):
+    """The current stream of the current device, on which the calls run and their
+    tensors live.  (The raw getters: the Stream object that
+    torch.cuda.current_stream builds costs more than a launch.)"""
+    dev = -1
     for t in ts:
         if t is not None:
-            if not t.is_cuda:
+            d = t.get_device()
+            if d < 0:
                 raise ValueError("libbq works on CUDA tensors only")
-            if t.device.index != here:
+            if dev < 0:
+                dev = torch._C._cuda_getDevice()
+            if d != dev:
                 raise ValueError("tensors must be on the current CUDA device")
-    return here
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _need(t, dtype, numel, what):
-    if t is not None and (t.dtype != dtype or not t.is_contiguous() or t.numel() < numel):
+    if t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of at least {numel} elements")
 
 
 def _need_rows(t, rows, cols, what):
     """bf16 [rows, cols] with unit column stride (the row stride may exceed cols)."""
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+    if (t.dtype is not _torch().bfloat16 or t.shape != (rows, cols)
+            or (cols > 1 and t.stride(1) != 1)):
         raise ValueError(f"{what} must be a bf16 [{rows}, {cols}] tensor with unit column stride")
-    if str(t.dtype) != "torch.bfloat16":
-        raise ValueError(f"{what} must be bf16")
 
 
 def _ld(t):
@@ -622,18 +635,22 @@ def act_quant_int8(x, q=None, scale=None, status=None):
     exceed K): returns (q int8 [M, K], scale fp32 [M]), q * scale ~ x.  Also the
     quantizer of a weight [N, K] with one scale per output channel."""
     torch = _torch()
-    _device_index(torch, x, q, scale, status)
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    stream = _here(torch, x, q, scale, status)
+    if x.dtype is not torch.bfloat16 or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x must be a bf16 [M, K] tensor with unit column stride")
     M, K = x.shape
     if q is None:
         q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    else:
+        _need(q, torch.int8, M * K, "q")
     if scale is None:
         scale = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _need(q, torch.int8, M * K, "q")
-    _need(scale, torch.float32, M, "scale")
-    _check(lib().bq_act_quant_int8(x.data_ptr(), M, K, _ld(x), q.data_ptr(), scale.data_ptr(),
-                                   _ptr(status), _stream()), "bq_act_quant_int8")
+    else:
+        _need(scale, torch.float32, M, "scale")
+    st = lib().bq_act_quant_int8(x.data_ptr(), M, K, _ld(x), q.data_ptr(), scale.data_ptr(),
+                                 None if status is None else status.data_ptr(), stream)
+    if st:
+        raise BqError(st, "bq_act_quant_int8")
     return q, scale
 
 
@@ -644,7 +661,7 @@ def gemm_int8_int8(a_q, a_scale, b, b_scale, M, N, K, y=None, bias=None, residua
     output channel (act_quant_int8).  batch: as in gemm; its scale strides
     step the fp32 scales.  config: GemmConfig or None (auto)."""
     torch = _torch()
-    _device_index(torch, a_q, a_scale, b, b_scale, y, bias, residual)
+    stream = _here(torch, a_q, a_scale, b, b_scale, y, bias, residual)
     count, sa, ssa, sb, ssb, sy, sr = 1, 0, 0, 0, 0, 0, 0
     if batch is not None:
         count = int(batch["count"])
@@ -655,36 +672,39 @@ def gemm_int8_int8(a_q, a_scale, b, b_scale, M, N, K, y=None, bias=None, residua
     _need(b, torch.int8, N * K + more * sb, "b")
     _need(a_scale, torch.float32, M + more * (ssa // 4), "a_scale")
     _need(b_scale, torch.float32, N + more * (ssb // 4), "b_scale")
-    _need(bias, torch.bfloat16, N, "bias")
     if y is None:
-        y = torch.empty((M, N) if batch is None else (count, M, N), dtype=torch.bfloat16,
-                        device=a_q.device)
-    _need(y, torch.bfloat16, M * N + more * (sy // 2), "y")
-    ld = 0
+        y = torch.empty((M, N) if batch is None else (count, M, N), dtype=torch.bfloat16, device=a_q.device)
+    else:
+        _need(y, torch.bfloat16, M * N + more * (sy // 2), "y")
+    L = lib()
+    if (bias is None and residual is None and alpha == 1.0 and act == BQ_ACT_NONE
+            and batch is None and config is None):
+        st = L.bq_gemm_int8_int8(a_q.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
+                                 b_scale.data_ptr(), M, N, K, y.data_ptr(), stream)
+        if st:
+            raise BqError(st, "bq_gemm_int8_int8")
+        return y
+    epi = Epilogue(None, None, 0, alpha, act, None, None)
+    if bias is not None:
+        _need(bias, torch.bfloat16, N, "bias")
+        epi.bias = bias.data_ptr()
     if residual is not None:
         if batch is None:
             _need_rows(residual, M, N, "residual")
-            ld = _ld(residual)
+            epi.ld_residual = _ld(residual)
         else:
-            if residual.dtype != torch.bfloat16 or residual.dim() < 2 or residual.stride(-1) != 1:
+            if (residual.dtype is not torch.bfloat16 or residual.dim() < 2
+                    or residual.stride(-1) != 1):
                 raise ValueError("residual must be bf16 with unit column stride")
-            ld = residual.stride(-2)
-    plain = (bias is None and residual is None and alpha == 1.0 and act == BQ_ACT_NONE
-             and batch is None and config is None)
-    if plain:
-        _check(lib().bq_gemm_int8_int8(a_q.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
-                                       b_scale.data_ptr(), M, N, K, y.data_ptr(), _stream()),
-               "bq_gemm_int8_int8")
-        return y
-    epi = Epilogue(bias.data_ptr() if bias is not None else None,
-                   residual.data_ptr() if residual is not None else None, ld, float(alpha),
-                   int(act), None, None)
+            epi.ld_residual = residual.stride(-2)
+        epi.residual = residual.data_ptr()
     bt = None if batch is None else ctypes.byref(Batch(count, sa, ssa, sb, ssb, sy, sr))
-    _check(lib().bq_gemm_int8_int8_epilogue(
+    st = L.bq_gemm_int8_int8_epilogue(
         a_q.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), M, N, K,
-        y.data_ptr(), ctypes.byref(epi), bt,
-        None if config is None else ctypes.byref(config), _stream()),
-        "bq_gemm_int8_int8_epilogue")
+        y.data_ptr(), ctypes.byref(epi), bt, None if config is None else ctypes.byref(config),
+        stream)
+    if st:
+        raise BqError(st, "bq_gemm_int8_int8_epilogue")
     return y
 
 
@@ -701,48 +721,52 @@ def gemm_gated(weight_kind, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, M, N, K, y=
     h is written when write_y is False.  Returns h, or a tuple (h or None, [q, sf],
     [gu]) when quantize_out or keep_projections ask for more."""
     torch = _torch()
-    _device_index(torch, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, y, gu, q_out, sf_out)
+    stream = _here(torch, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, y, gu, q_out, sf_out)
     if not write_y and not quantize_out:
         raise ValueError("write_y=False needs quantize_out=True")
-    dev = a_q.device
     if weight_kind == W_INT8:
-        _need(a_q, torch.int8, M * K, "a_q")
-        _need(a_sf, torch.float32, M, "a_sf")
-        for w, s in ((b_gate, gate_sf), (b_up, up_sf)):
-            _need(w, torch.int8, N * K, "weights")
-            _need(s, torch.float32, N, "weight scales")
+        code, scale, na, nw, nws = torch.int8, torch.float32, M, N * K, N
     else:
-        _need(a_q, torch.uint8, M * K, "a_q")
-        _need(a_sf, torch.uint8, sf_bytes(M, K), "a_sf")
-        nb = N * K // 2 if weight_kind == W_MXFP4 else N * K
-        for w, s in ((b_gate, gate_sf), (b_up, up_sf)):
-            _need(w, torch.uint8, nb, "weights")
-            _need(s, torch.uint8, sf_bytes(N, K), "weight scales")
+        code = scale = torch.uint8
+        ka = -(-K // 128) * 512
+        na, nws = -(-M // 128) * ka, -(-N // 128) * ka
+        nw = N * K // 2 if weight_kind == W_MXFP4 else N * K
+    _need(a_q, code, M * K, "a_q")
+    _need(a_sf, scale, na, "a_sf")
+    _need(b_gate, code, nw, "b_gate")
+    _need(gate_sf, scale, nws, "gate_sf")
+    _need(b_up, code, nw, "b_up")
+    _need(up_sf, scale, nws, "up_sf")
+    epi = GatedEpilogue(alpha, act, None, None, None)
     if not write_y:
         y = None
     elif y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    if keep_projections and gu is None:
-        gu = torch.empty((M, 2 * N), dtype=torch.bfloat16, device=dev)
-    if quantize_out:
-        if q_out is None:
-            q_out = torch.empty((M, N), dtype=torch.uint8, device=dev)
-        if sf_out is None:
-            sf_out = torch.empty((max(sf_bytes(M, N), 1),), dtype=torch.uint8, device=dev)
-        _need(q_out, torch.uint8, M * N, "q_out")
-        _need(sf_out, torch.uint8, sf_bytes(M, N), "sf_out")
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device)
     else:
-        q_out = sf_out = None
-    _need(y, torch.bfloat16, M * N, "y")
-    _need(gu, torch.bfloat16, 2 * M * N, "gu")
-    epi = GatedEpilogue(float(alpha), int(act), None if gu is None else gu.data_ptr(),
-                        None if q_out is None else q_out.data_ptr(),
-                        None if sf_out is None else sf_out.data_ptr())
-    _check(lib().bq_gemm_gated(
-        int(weight_kind), a_q.data_ptr(), a_sf.data_ptr(), b_gate.data_ptr(), gate_sf.data_ptr(),
+        _need(y, torch.bfloat16, M * N, "y")
+    if gu is not None:
+        _need(gu, torch.bfloat16, 2 * M * N, "gu")
+    elif keep_projections:
+        gu = torch.empty((M, 2 * N), dtype=torch.bfloat16, device=a_q.device)
+    if gu is not None:
+        epi.gu_out = gu.data_ptr()
+    if quantize_out:
+        nsf = -(-M // 128) * -(-N // 128) * 512
+        if q_out is None:
+            q_out = torch.empty((M, N), dtype=torch.uint8, device=a_q.device)
+        else:
+            _need(q_out, torch.uint8, M * N, "q_out")
+        if sf_out is None:
+            sf_out = torch.empty((max(nsf, 1),), dtype=torch.uint8, device=a_q.device)
+        else:
+            _need(sf_out, torch.uint8, nsf, "sf_out")
+        epi.q_out, epi.sf_out = q_out.data_ptr(), sf_out.data_ptr()
+    st = lib().bq_gemm_gated(
+        weight_kind, a_q.data_ptr(), a_sf.data_ptr(), b_gate.data_ptr(), gate_sf.data_ptr(),
         b_up.data_ptr(), up_sf.data_ptr(), M, N, K, None if y is None else y.data_ptr(),
-        ctypes.byref(epi), None if config is None else ctypes.byref(config), _stream()),
-        "bq_gemm_gated")
+        ctypes.byref(epi), None if config is None else ctypes.byref(config), stream)
+    if st:
+        raise BqError(st, "bq_gemm_gated")
     if not quantize_out and gu is None:
         return y
     return (y,) + ((q_out, sf_out) if quantize_out else ()) + ((gu,) if gu is not None else ())
@@ -758,27 +782,34 @@ def gated_grad_quant(dh, gu, act=BQ_GATE_SILU, stochastic=False, seed=0, out=Non
     q_row = sf_row = q_t = sf_t = None
     if out is not None:
         q_row, sf_row, q_t, sf_t = out
-    _device_index(torch, dh, gu, q_row, sf_row, q_t, sf_t, d, status)
+    stream = _here(torch, dh, gu, q_row, sf_row, q_t, sf_t, d, status)
     if dh.dim() != 2:
         raise ValueError("dh must be a bf16 [M, N] tensor")
     M, N = dh.shape
     _need_rows(dh, M, N, "dh")
     _need_rows(gu, M, 2 * N, "gu")
-    n_row, n_t = max(sf_bytes(M, 2 * N), 1), max(sf_bytes(2 * N, M) if M else 1, 1)
+    n_row = max(-(-M // 128) * -(-2 * N // 128) * 512, 1)  # both scale buffers have as many atoms
     if out is None:
-        u8 = dict(dtype=torch.uint8, device=dh.device)
-        q_row, sf_row = torch.empty((M, 2 * N), **u8), torch.empty((n_row,), **u8)
-        q_t, sf_t = torch.empty((2 * N, M), **u8), torch.empty((n_t,), **u8)
-    _need(q_row, torch.uint8, 2 * M * N, "q_row")
-    _need(q_t, torch.uint8, 2 * M * N, "q_t")
-    _need(sf_row, torch.uint8, n_row, "sf_row")
-    _need(sf_t, torch.uint8, n_t, "sf_t")
-    _need(d, torch.bfloat16, 2 * M * N, "d")
-    _check(lib().bq_gated_grad_quant(
-        dh.data_ptr(), _ld(dh), gu.data_ptr(), _ld(gu), M, N, int(act),
+        u8 = torch.uint8
+        dev = dh.device
+        q_row = torch.empty((M, 2 * N), dtype=u8, device=dev)
+        sf_row = torch.empty((n_row,), dtype=u8, device=dev)
+        q_t = torch.empty((2 * N, M), dtype=u8, device=dev)
+        sf_t = torch.empty((n_row,), dtype=u8, device=dev)
+    else:
+        _need(q_row, torch.uint8, 2 * M * N, "q_row")
+        _need(q_t, torch.uint8, 2 * M * N, "q_t")
+        _need(sf_row, torch.uint8, n_row, "sf_row")
+        _need(sf_t, torch.uint8, n_row, "sf_t")
+    if d is not None:
+        _need(d, torch.bfloat16, 2 * M * N, "d")
+    st = lib().bq_gated_grad_quant(
+        dh.data_ptr(), _ld(dh), gu.data_ptr(), _ld(gu), M, N, act,
         BQ_ROUND_STOCHASTIC if stochastic else BQ_ROUND_NEAREST, int(seed) & (2 ** 64 - 1),
         q_row.data_ptr(), sf_row.data_ptr(), q_t.data_ptr(), sf_t.data_ptr(),
-        None if d is None else d.data_ptr(), _ptr(status), _stream()), "bq_gated_grad_quant")
+        None if d is None else d.data_ptr(), None if status is None else status.data_ptr(), stream)
+    if st:
+        raise BqError(st, "bq_gated_grad_quant")
     return q_row, sf_row, q_t, sf_t
 
 

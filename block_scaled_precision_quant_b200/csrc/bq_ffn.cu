@@ -115,7 +115,8 @@ int output_map(CUtensorMap* m, const void* y, int64_t M, int64_t N, int64_t ld, 
 struct Plan {
   bool pair = false;  // 256-row tiles on pairs of SMs (lin_pair.cuh), else lin_swap.cuh
   int bn = 0;         // swap: activation rows of a tile; pair: weight rows (256)
-  int splits = 1;  // K slices (CTAs of a cluster)
+  int splits = 1;     // swap: K slices (CTAs of a cluster)
+  int occ = 1;        // swap: CTAs an SM holds
   int64_t tiles_p = 0, tiles_q = 0, tiles = 0;
   int kt = 0;
 };
@@ -140,43 +141,84 @@ int check_config(const bq_gemm_config* cfg) {
   return BQ_OK;
 }
 
+// Estimated microseconds of the two schedules, fitted to sweeps over 1 to 2048
+// rows, 512 to 16384 outputs and K of 512 to 8192 (within about 15 % of them).
+// What either spends its time on is filling shared memory, about 105 KB a
+// microsecond and SM, so a tile's cost is the bytes of its K blocks.
+//   swap: launch, first copies and outputs 3.8 us, longer by the tile's rows;
+//         a split adds the exchange (int8 41 x 4608 x 1536: 6.4 us unsplit, 6.1 in
+//         4 slices; 41 x 1536 x 6144: 14.5 and 6.7 in 8; gated 41 x 6144 x 1536:
+//         10.4 and 8.6 in 2, 9.3 in 4).
+//   pair: 6.3 us (gated 7.5) and 0.29 us a K block of 256 x 256 (int8 256 x 4096 x
+//         4096: 15.6 us, 12.0 as 64-row tiles; 1024 x 4096 x 4096: 17.8, 28 as
+//         128-row tiles; 512 x 1024 x 1024: 8.4, 5.6 as 64-row tiles).
+double swap_us(int bn, int64_t tiles, int splits, int kt, bool gated, int num_sms) {
+  const double ctas = static_cast<double>(tiles * splits);
+  const double share =  // CTAs that share an SM's bandwidth
+      ctas <= 2.0 * num_sms ? (ctas <= num_sms ? 1.0 : 2.0) : ctas / num_sms;
+  const double chunk_kb = (gated ? 32 : 16) + bn / 8.0;
+  return 3.8 + bn / 128.0 * 0.8 * (gated ? 2 : 1) + share * kt / splits * chunk_kb / 105.0 +
+         (splits > 1 ? bn / 64.0 * 1.6 : 0.0);
+}
+
+double pair_us(int64_t tiles, int kt, bool gated, int num_sms) {
+  const int64_t waves = ceil_div(tiles, num_sms / 2);
+  return (gated ? 7.5 : 6.3) + static_cast<double>(waves) * (kt * 0.29 + (gated ? 1.0 : 0.5));
+}
+
 int make_plan(Kind kind, bool gated, int64_t M, int64_t N, int64_t K, int64_t batch,
               const bq_gemm_config* cfg, int num_sms, Plan* p) {
   const bq_gemm_config c = cfg ? *cfg : bq_gemm_config{0, 0, -1, BQ_SPLIT_AUTO, 0, 0};
   // MX tiles start at the first row of a scale atom (lin_swap.cuh)
   if (kind != kInt8 && c.block_n != 0 && c.block_n < 128 && M > c.block_n) return BQ_ERR_INVALID;
   p->kt = static_cast<int>(ceil_div(K, 128));
-  const bool swap_asked = c.swap_ab == 1 || c.cta_pair == 1 || c.split_k > 0 || c.block_n == 32 ||
-                          c.block_n == 64 || c.block_n == 128;
-  p->pair = c.swap_ab == 0 || c.cta_pair == 2 || c.block_n == 256 || (!swap_asked && M > 128);
+  const bool pair_asked = c.swap_ab == 0 || c.cta_pair == 2 || c.block_n == 256;
+  const bool swap_asked = !pair_asked && (c.swap_ab == 1 || c.cta_pair == 1 || c.split_k > 0 ||
+                                          c.block_n != 0);
+  const int64_t pair_p = ceil_div(M, 256), pair_q = ceil_div(N, gated ? 128 : 256);
+  const int64_t tiles_p = ceil_div(N, 128);
+  double best = 1e30;
+  for (int bn = 32; bn <= 128 && !pair_asked; bn *= 2) {
+    if (c.block_n ? bn != c.block_n
+                  : (bn < 128 && M > bn && (bn == 32 || kind != kInt8)) || (bn > 32 && M <= bn / 2))
+      continue;
+    const int64_t tiles_q = ceil_div(M, bn), tiles = tiles_p * tiles_q * batch;
+    for (int s = c.split_k ? c.split_k : 1; s <= (c.split_k ? c.split_k : kMaxSplit); s *= 2) {
+      // a split's clusters find a place at once up to about nine tenths of the SMs
+      if (!c.split_k && s > 1 && (p->kt / s < 2 || tiles * s * 10 > num_sms * 18)) break;
+      const double us = swap_us(bn, tiles, s, p->kt, gated, num_sms);
+      if (us >= best) continue;
+      best = us;
+      p->bn = bn;
+      p->splits = std::min(s, p->kt);
+      p->tiles_p = tiles_p;
+      p->tiles_q = tiles_q;
+    }
+  }
+  p->pair = pair_asked ||
+            (!swap_asked && M > 64 &&
+             pair_us(pair_p * pair_q * batch, p->kt, gated, num_sms) < best);
   if (p->pair) {
     p->bn = 256;
-    p->tiles_p = ceil_div(M, 256);
-    p->tiles_q = ceil_div(N, gated ? 128 : 256);
-    p->tiles = p->tiles_p * p->tiles_q * batch;
-    return p->tiles > 0x7FFFFFFF ? BQ_ERR_SHAPE : BQ_OK;
+    p->splits = 1;
+    p->tiles_p = pair_p;
+    p->tiles_q = pair_q;
   }
-  p->bn = c.block_n ? c.block_n : (M <= 32 ? 32 : M <= 64 ? 64 : 128);
-  p->tiles_p = ceil_div(N, 128);
-  p->tiles_q = ceil_div(M, p->bn);
   p->tiles = p->tiles_p * p->tiles_q * batch;
-  int s = c.split_k;
-  if (s == 0) {
-    s = 1;
-    while (s < kMaxSplit && p->tiles * (s + 1) <= num_sms && p->kt / (s + 1) >= 2) ++s;
-  }
-  p->splits = std::min(s, p->kt);
-  if (p->tiles * p->splits > 0x7FFFFFFF) return BQ_ERR_SHAPE;
-  return BQ_OK;
+  // One CTA to an SM has twice the stages: it streams faster where there are no
+  // more tiles than SMs (int8 512 x 4096 x 4096 in 128-row tiles: 14.0 us, 16.1
+  // with two); two take the tiles beyond that (1024 x 4096 x 4096: 28.1 and 21.5).
+  p->occ = p->splits == 1 && p->tiles <= num_sms ? 1 : 2;
+  return p->tiles * p->splits > 0x7FFFFFFF ? BQ_ERR_SHAPE : BQ_OK;
 }
 
 // ---------------------------------------------------------------- launches --
 
-template <int BN, bool I8, bool GATED>
+template <int BN, bool I8, bool GATED, int OCC>
 int launch_swap(const Plan& pl, const CUtensorMap& w0, const CUtensorMap& w1,
                 const CUtensorMap& ta, const bq::FfnArgs& a, int dev, bq_stream_t stream) {
-  using L = bq::SwapSmem<BN, I8, GATED>;
-  auto kern = bq::lin_swap_kernel<BN, I8, GATED>;
+  using L = bq::SwapSmem<BN, I8, GATED, OCC>;
+  auto kern = bq::lin_swap_kernel<BN, I8, GATED, OCC>;
   static bool ready[bqh::kMaxDevices] = {};
   if (!ready[dev]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
@@ -211,10 +253,18 @@ int launch_pair(const Plan& pl, const Map& ta, const Map& w0, const Map& w1, con
 template <bool I8, bool GATED>
 int run_swap(const Plan& pl, const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& ta,
              const bq::FfnArgs& a, int dev, bq_stream_t stream) {
+  if (pl.occ == 2) {
+    switch (pl.bn) {
+      case 32: return launch_swap<32, I8, GATED, 2>(pl, w0, w1, ta, a, dev, stream);
+      case 64: return launch_swap<64, I8, GATED, 2>(pl, w0, w1, ta, a, dev, stream);
+      default:
+        if constexpr (!GATED) return launch_swap<128, I8, GATED, 2>(pl, w0, w1, ta, a, dev, stream);
+    }
+  }
   switch (pl.bn) {
-    case 32: return launch_swap<32, I8, GATED>(pl, w0, w1, ta, a, dev, stream);
-    case 64: return launch_swap<64, I8, GATED>(pl, w0, w1, ta, a, dev, stream);
-    default: return launch_swap<128, I8, GATED>(pl, w0, w1, ta, a, dev, stream);
+    case 32: return launch_swap<32, I8, GATED, 1>(pl, w0, w1, ta, a, dev, stream);
+    case 64: return launch_swap<64, I8, GATED, 1>(pl, w0, w1, ta, a, dev, stream);
+    default: return launch_swap<128, I8, GATED, 1>(pl, w0, w1, ta, a, dev, stream);
   }
 }
 

@@ -8,7 +8,7 @@
 // stand, each CTA copies them from TMEM into its shared memory (over the
 // operand stages, which are done with), [weight][row m][128 outputs n], and
 // after a cluster barrier all warps of the S CTAs share out the rows: a warp
-// takes a row, a lane four outputs, sums the S slices in rank order through
+// takes a row, a lane four outputs, sums the S slices in a fixed order through
 // distributed shared memory, and finishes the outputs (scales, bias,
 // activation, product, residual, quantization), so the arithmetic after the
 // sum is spread over the cluster and every store is a row's contiguous 256
@@ -33,14 +33,18 @@ namespace bq {
 constexpr int kSwapThreads = 320;
 constexpr int kSwapWarps = kSwapThreads / 32;
 
-template <int BN, bool I8, bool GATED>
+// OCC: CTAs an SM holds.  One with all the shared memory streams large weights;
+// two with half each leave more places for the clusters of a split (an SM of
+// its own for each CTA of a cluster is hard to find: of 48 clusters of three
+// only some fit at once) and let a kernel's start overlap the one before.
+template <int BN, bool I8, bool GATED, int OCC>
 struct SwapSmem {
   static constexpr int kWeights = GATED ? 2 : 1;
   static constexpr int kBytesW = kBlockP * kBlockK;  // one weight's 128 x 128 tile
   static constexpr int kBytesA = BN * kBlockK;
   static constexpr int kBytesSf = I8 ? 0 : (kWeights + 1) * kSfAtom;
   static constexpr int kStageTiles = kWeights * kBytesW + kBytesA;  // 1024-byte multiple
-  static constexpr int kFit = (200 * 1024) / (kStageTiles + kBytesSf);
+  static constexpr int kFit = (OCC == 2 ? 108 * 1024 : 200 * 1024) / (kStageTiles + kBytesSf);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kOffSf = kStages * kStageTiles;
   static constexpr int kOffBar = kOffSf + kStages * kBytesSf;
@@ -57,10 +61,12 @@ struct SwapSmem {
   static constexpr int kPart = BN * kBlockP * 4;  // one weight's sums, over the stages
   static_assert(kTmemUsed <= 512, "TMEM budget");
   static_assert(kWeights * kPart <= kOffSf, "the sums overlay the operand stages");
-  static_assert(kBytes <= 232448, "shared memory budget");
+  static_assert(kBytes <= (OCC == 2 ? 115712 : 232448), "shared memory budget");
+  static_assert(OCC * kTmemCols <= 512, "TMEM of co-resident CTAs");
 };
 
-// Four consecutive sums of row m of weight w, all slices in rank order.
+// Four consecutive sums of one row and weight, at this shared-memory address in
+// each CTA of the cluster, all slices in rank order.
 template <bool I8>
 __device__ __forceinline__ void sum_slices(uint32_t local, int S, float (&v)[4]) {
   if constexpr (I8) {
@@ -88,12 +94,12 @@ __device__ __forceinline__ void sum_slices(uint32_t local, int S, float (&v)[4])
   }
 }
 
-template <int BN, bool I8, bool GATED>
-__global__ void __launch_bounds__(kSwapThreads, 1)
+template <int BN, bool I8, bool GATED, int OCC>
+__global__ void __launch_bounds__(kSwapThreads, OCC)
     lin_swap_kernel(const __grid_constant__ CUtensorMap tm_w0,
                     const __grid_constant__ CUtensorMap tm_w1,
                     const __grid_constant__ CUtensorMap tm_a, const FfnArgs a) {
-  using L = SwapSmem<BN, I8, GATED>;
+  using L = SwapSmem<BN, I8, GATED, OCC>;
   constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -130,6 +136,13 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     tma_prefetch_desc(&tm_w0);
     tma_prefetch_desc(&tm_a);
     if (GATED) tma_prefetch_desc(&tm_w1);
+    // The first weight tiles do not wait for the kernel before, nor for the
+    // set-up that follows.
+    for (int st = 0; st < kStages && kt0 + st < kt1; ++st) {
+      mbar_arrive_expect_tx(&full[st], a.w_tile_bytes);
+      tma_load_3d(smem + st * L::kStageTiles, &tm_w0, &full[st], (kt0 + st) * kBlockK, n0,
+                  a.p_batched ? b : 0);
+    }
   }
   if (warp == 1) tmem_alloc(tmem_slot, L::kTmemCols);
   tc_fence_before();
@@ -149,7 +162,12 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int kt = kt0; kt < kt1; ++kt) {
+      int kt = kt0;
+      if (warp == 0) {  // the tiles issued above
+        kt = min(kt0 + kStages, kt1);
+        phase = 1;
+      }
+      for (; kt < kt1; ++kt) {
         if (!mbar_wait(&empty[stage], phase ^ 1, a.err, abort_flag, kWaitProdEmpty)) {
           ok = false;
           break;
@@ -257,7 +275,10 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
   // may also still read or write the outputs.
   griddep_wait();
   tc_fence_before();
-  cluster_sync_all();
+  if (S > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
 
   // ------------------------------------------------------------- outputs --
   {
@@ -274,20 +295,30 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                        : a.alpha;
       bias[j] = (!GATED && a.bias && nok) ? __bfloat162float(a.bias[n + j]) : 0.0f;
     }
-    const uint32_t part = smem_u32(smem) + static_cast<uint32_t>(16 * lane);
     const int64_t groups = a.N >> 5, katoms = (groups + 3) >> 2;
+    // One row a warp and round, in code that is short: it runs once, from a cold
+    // instruction cache (four rows a round, fetched together, took 0.5 to 2 us
+    // longer on 41 x 1536 x 6144 split eight ways and gained nothing elsewhere).
 #pragma unroll 1
     for (int r = rank * kSwapWarps + warp; r < mt; r += S * kSwapWarps) {
       const int m = m0 + r;
+      const float sa = I8 ? __ldg(a.sa + b * a.sa_bstride + m) : 1.0f;
       float v[2][4];
 #pragma unroll
-      for (int w = 0; w < L::kWeights; ++w)
-        sum_slices<I8>(part + static_cast<uint32_t>(w * L::kPart + r * kBlockP * 4), S, v[w]);
-      const float sa = I8 ? __ldg(a.sa + b * a.sa_bstride + m) : 1.0f;
+      for (int w = 0; w < L::kWeights; ++w) {
+        const uint32_t at = static_cast<uint32_t>(w * L::kPart + r * kBlockP * 4 + 16 * lane);
+        if (S == 1) {
+          const uint4 p = *reinterpret_cast<const uint4 *>(smem + at);
+          const uint32_t t[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-      for (int w = 0; w < L::kWeights; ++w)
+          for (int j = 0; j < 4; ++j)
+            v[w][j] = I8 ? __int2float_rn(static_cast<int>(t[j])) : __uint_as_float(t[j]);
+        } else {
+          sum_slices<I8>(smem_u32(smem) + at, S, v[w]);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[w][j] *= I8 ? sa * sw[w][j] : sw[w][j];
+      }
       float t[4];
       if constexpr (GATED) {
         if (a.gu && nok) {
@@ -353,7 +384,10 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     }
   }
   // No CTA leaves while a peer still reads its sums.
-  cluster_sync_all();
+  if (S > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();

@@ -110,10 +110,27 @@ def test_binding_refusals():
 
 
 def test_plans():
-    c = bq.ffn_plan(41, 4608, 1536)
-    assert c.swap_ab == 1 and c.block_n == 64 and 36 * c.split_k <= 148 and c.split_k > 1
-    c = bq.ffn_plan(1, 16384, 8192, weight_kind=bq.W_FP8BLK32, gated=True)
-    assert c.swap_ab == 1 and c.block_n == 32 and c.split_k == 1
+    def p(M, N, K, **kw):
+        c = bq.ffn_plan(M, N, K, **kw)
+        return c.swap_ab, c.block_n, c.split_k
+
+    # decode: one tile of rows, split where K is long and SMs are left
+    assert p(1, 4608, 1536)[:2] == (1, 32)
+    assert p(41, 1536, 6144) == (1, 64, 8)
+    assert p(41, 6144, 1536, weight_kind=bq.W_MXFP4, gated=True) == (1, 64, 2)
+    # large weights: every SM streams
+    assert p(16, 16384, 8192)[2] * 128 >= 128
+    assert p(16, 16384, 8192, weight_kind=bq.W_FP8BLK32, gated=True) == (1, 32, 1)
+    # between: tiles of one SM while pairs would leave most of them idle
+    assert p(512, 1024, 1024) == (1, 64, 1)
+    assert p(200, 512, 8192) == (1, 64, 8)
+    # many rows: pairs of SMs
+    for kw in (dict(), dict(gated=True), dict(gated=True, weight_kind=bq.W_MXFP8)):
+        assert p(8192, 8192, 8192, **kw) == (0, 256, 1)
+    for kind in (bq.W_MXFP4, bq.W_FP8BLK32, bq.W_MXFP8):  # short MX tiles hold all rows
+        for M in range(1, 400, 7):
+            sw, bn, _ = p(M, 768, 2048, weight_kind=kind, gated=True)
+            assert sw == 0 or bn == 128 or M <= bn
     # an MX tile shorter than a scale atom holds all rows
     for M, bn, ok in ((32, 32, True), (33, 32, False), (64, 64, True), (65, 64, False),
                       (300, 128, True)):
