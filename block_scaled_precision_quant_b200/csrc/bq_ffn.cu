@@ -509,7 +509,7 @@ int bq_gated_grad_quant(const void* dh_bf16, int64_t ld_dh, const void* gu_bf16,
   if (M < 0 || M % 32 != 0 || N <= 0 || N % 32 != 0 || ld_dh < N || ld_gu < 2 * N)
     return BQ_ERR_SHAPE;
   const int64_t groups = ceil_div(M, 128) * 4, tiles = ceil_div(N, 64);
-  if (groups > 0x7FFFFFFF || ceil_div(tiles, 8) > 65535) return BQ_ERR_SHAPE;
+  if (groups > 0x7FFFFFFF || ceil_div(tiles, 2) > 65535) return BQ_ERR_SHAPE;
   if (M > 0) {
     if (!dh_bf16 || !gu_bf16 || !q_row || !sf_row || !q_t || !sf_t) return BQ_ERR_NULL;
     if (!aligned(dh_bf16, 16) || !aligned(gu_bf16, 16) || ld_dh % 8 != 0 || ld_gu % 8 != 0 ||
@@ -519,17 +519,32 @@ int bq_gated_grad_quant(const void* dh_bf16, int64_t ld_dh, const void* gu_bf16,
   Device dev;
   const int st = bqh::current_device(&dev);
   if (st != BQ_OK || M == 0) return st;
-  const bool sr = rounding == BQ_ROUND_STOCHASTIC;
-  auto kern = act == BQ_GATE_SILU ? (sr ? bq::gated_grad_kernel<bq::kGateSilu, true>
-                                        : bq::gated_grad_kernel<bq::kGateSilu, false>)
-                                  : (sr ? bq::gated_grad_kernel<bq::kGateGelu, true>
-                                        : bq::gated_grad_kernel<bq::kGateGelu, false>);
+  const auto* dh = static_cast<const __nv_bfloat16*>(dh_bf16);
+  const auto* gu = static_cast<const __nv_bfloat16*>(gu_bf16);
+  auto *qr = static_cast<uint8_t*>(q_row), *sr = static_cast<uint8_t*>(sf_row);
+  auto *qt = static_cast<uint8_t*>(q_t), *st8 = static_cast<uint8_t*>(sf_t);
+  auto* d = static_cast<__nv_bfloat16*>(d_bf16);
+  if (rounding == BQ_ROUND_NEAREST) {
+    auto kern = act == BQ_GATE_SILU ? bq::gated_grad_rne_kernel<bq::kGateSilu>
+                                    : bq::gated_grad_rne_kernel<bq::kGateGelu>;
+    static bool ready[bqh::kMaxDevices][2] = {};
+    if (!ready[dev.index][act]) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               bq::GradSmem::kBytes) != cudaSuccess)
+        return BQ_ERR_CUDA;
+      ready[dev.index][act] = true;
+    }
+    return launch(kern,
+                  dim3(static_cast<unsigned>(ceil_div(M, 128)),
+                       static_cast<unsigned>(ceil_div(N, 128))),
+                  256, bq::GradSmem::kBytes, 1, stream, dh, ld_dh, gu, ld_gu, M, N, qr, sr, qt, st8, d,
+                  d_status);
+  }
+  auto kern = act == BQ_GATE_SILU ? bq::gated_grad_sr_kernel<bq::kGateSilu>
+                                  : bq::gated_grad_sr_kernel<bq::kGateGelu>;
   return launch(kern, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(ceil_div(tiles, 8))),
-                256, 0, 1, stream, static_cast<const __nv_bfloat16*>(dh_bf16), ld_dh,
-                static_cast<const __nv_bfloat16*>(gu_bf16), ld_gu, M, N, tiles,
-                static_cast<uint8_t*>(q_row), static_cast<uint8_t*>(sf_row),
-                static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(sf_t),
-                static_cast<__nv_bfloat16*>(d_bf16), d_status, seed);
+                256, 0, 1, stream, dh, ld_dh, gu, ld_gu, M, N, tiles, qr, sr, qt, st8, d, d_status,
+                seed);
 }
 
 int bq_ffn_plan(int weight_kind, int gated, int64_t M, int64_t N, int64_t K, int64_t batch,

@@ -43,7 +43,6 @@ __device__ __forceinline__ void gate_grad(float dh, float g, float u, float &dg,
 // row r0 + l in w (column 2 i in the low half of word i), zeros where there is
 // nothing.  c0: the tile's first column in d (C = 2 F columns), ncols = 32 or 64
 // of them exist.  rows_ok: the 32 rows exist.
-template <bool SR>
 __device__ __forceinline__ void dual_quant_tile(const uint32_t (&w)[32], int64_t R, int64_t C,
                                                 int64_t r0, int64_t c0, int ncols, bool rows_ok,
                                                 int lane, uint8_t *st, uint8_t *q_row,
@@ -101,20 +100,14 @@ __device__ __forceinline__ void dual_quant_tile(const uint32_t (&w)[32], int64_t
     const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
     const float t0 = __fmul_rn(x0, inv0), t1 = __fmul_rn(x1, inv1);    // along the rows
     const float r0f = __fmul_rn(x0, rinv), r1f = __fmul_rn(x1, rinv);  // along the columns
-    uint32_t pt, pr;
-    if constexpr (SR) {
-      if (i % 4 == 0)
-        rnd = philox4x64_10(static_cast<uint64_t>(row * C + c0 + 2 * i) >> 3, seed);
-      const uint32_t u0 = philox_draw(rnd, (2 * i) & 7), u1 = philox_draw(rnd, ((2 * i) & 7) + 1);
-      auto sr = [](float v, uint32_t u) {
-        return e5m2_sr(fminf(fmaxf(v, -57344.0f), 57344.0f), u);
-      };
-      pt = sr(t0, u0) | (sr(t1, u1) << 8);
-      pr = sr(r0f, u0) | (sr(r1f, u1) << 8);
-    } else {
-      pt = e5m2x2(t0, t1);
-      pr = e5m2x2(r0f, r1f);
-    }
+    if (i % 4 == 0)  // one Philox block serves 8 consecutive elements of a row
+      rnd = philox4x64_10(static_cast<uint64_t>(row * C + c0 + 2 * i) >> 3, seed);
+    const uint32_t u0 = philox_draw(rnd, (2 * i) & 7), u1 = philox_draw(rnd, ((2 * i) & 7) + 1);
+    auto sr = [](float v, uint32_t u) {
+      return e5m2_sr(fminf(fmaxf(v, -57344.0f), 57344.0f), u);
+    };
+    const uint32_t pt = sr(t0, u0) | (sr(t1, u1) << 8);
+    const uint32_t pr = sr(r0f, u0) | (sr(r1f, u1) << 8);
     st[(2 * i) * 32 + lane] = static_cast<uint8_t>(pt);
     st[(2 * i + 1) * 32 + lane] = static_cast<uint8_t>(pt >> 8);
     if (i % 2 == 0)
@@ -146,8 +139,8 @@ __device__ __forceinline__ void dual_quant_tile(const uint32_t (&w)[32], int64_t
 // bf16, row pitch 2 F (optional).  R % 32 == 0, F % 32 == 0.
 // grid.x = 32-row group (up to the scale padding), grid.y * 8 + warp = tile of 64
 // columns of F; a warp forms and quantizes its tile of dG, then that of dU.
-template <int ACT, bool SR>
-__global__ void __launch_bounds__(256, 2) gated_grad_kernel(
+template <int ACT>
+__global__ void __launch_bounds__(256, 2) gated_grad_sr_kernel(
     const __nv_bfloat16 *__restrict__ dh, int64_t ld_dh, const __nv_bfloat16 *__restrict__ gu,
     int64_t ld_gu, int64_t R, int64_t F, int64_t col_tiles, uint8_t *__restrict__ q_row,
     uint8_t *__restrict__ sf_row, uint8_t *__restrict__ q_t, uint8_t *__restrict__ sf_t,
@@ -193,15 +186,221 @@ __global__ void __launch_bounds__(256, 2) gated_grad_kernel(
           make_uint4(wu[4 * v], wu[4 * v + 1], wu[4 * v + 2], wu[4 * v + 3]);
     }
   }
-  dual_quant_tile<SR>(wg, R, C, r0, c0, ncols, rows_ok, lane, stage[warp], q_row, sf_row, q_t,
+  dual_quant_tile(wg, R, C, r0, c0, ncols, rows_ok, lane, stage[warp], q_row, sf_row, q_t,
                       sf_t, status, seed);
-  dual_quant_tile<SR>(wu, R, C, r0, F + c0, ncols, rows_ok, lane, stage[warp], q_row, sf_row, q_t,
+  dual_quant_tile(wu, R, C, r0, F + c0, ncols, rows_ok, lane, stage[warp], q_row, sf_row, q_t,
                       sf_t, status, seed);
   if (ct == col_tiles - 1) {  // scale padding behind the last column
     const int64_t katoms_t = ((R >> 5) + 3) >> 2, katoms_r = ((C >> 5) + 3) >> 2;
     for (int64_t g = C >> 5; g < katoms_r * 4; ++g) sf_row[sf_mma_offset(row, g, katoms_r)] = 127;
     for (int64_t c = C + lane; c < (C + 127) / 128 * 128; c += 32)
       sf_t[sf_mma_offset(c, r0 >> 5, katoms_t)] = 127;
+  }
+}
+
+// ---- round to nearest ------------------------------------------------------
+//
+// A block owns 128 rows x 128 columns of F and works on them three times, each
+// time with the ownership that needs no exchange between threads:
+//   1. eight columns of a row a thread (three 16-byte loads): dG and dU as bf16
+//      into two tiles in shared memory;
+//   2. 16 columns of a row a thread, two threads a group (one shuffle for its
+//      maximum): the row-wise codes, a row's 128 bytes by eight threads;
+//   3. two columns x 32 rows a thread, whole groups: the transposed codes, which
+//      turn around through the tiles' memory and leave as 128-byte lines.
+// 35 instructions an element instead of the 63 of a version that kept one
+// ownership and met by shuffles.  Floor: 6 bytes read and 4.1 written for each
+// element of F.
+struct GradSmem {
+  static constexpr int kTile = 128 * 256;      // [128 rows][128 bf16]
+  static constexpr int kOffSfr = 2 * kTile;    // [2][128 rows][4 groups]
+  static constexpr int kOffSft = kOffSfr + 1024;  // [2][128 columns][4 groups]
+  static constexpr int kBytes = kOffSft + 1024;
+};
+
+// Byte offset of 16-byte piece q (8 columns) of row r of a tile: the pieces of a
+// row's second half are swapped in pairs, so eight threads that read every second
+// piece of a row meet no bank twice.
+__device__ __forceinline__ uint32_t grad_at(int r, int q) {
+  return static_cast<uint32_t>(r * 256 + ((q ^ (q >> 3)) << 4));
+}
+
+// Byte offset of 16-byte piece q of row r of a [128][128]-byte tile, permuted so
+// that stores to every second row and loads of whole rows meet no bank twice.
+__device__ __forceinline__ uint32_t code_at(int r, int q) {
+  return static_cast<uint32_t>(r * 128 + ((q ^ ((r >> 1) & 7)) << 4));
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(256, 3) gated_grad_rne_kernel(
+    const __nv_bfloat16 *__restrict__ dh, int64_t ld_dh, const __nv_bfloat16 *__restrict__ gu,
+    int64_t ld_gu, int64_t R, int64_t F, uint8_t *__restrict__ q_row, uint8_t *__restrict__ sf_row,
+    uint8_t *__restrict__ q_t, uint8_t *__restrict__ sf_t, __nv_bfloat16 *__restrict__ d_out,
+    int *__restrict__ status) {
+  extern __shared__ __align__(128) uint8_t grad_smem[];
+  uint8_t *sm = grad_smem;
+  const int tid = threadIdx.x;
+  const int64_t C = 2 * F, b0 = static_cast<int64_t>(blockIdx.x) * 128;  // rows
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * 128;             // columns of F
+  const int ncols = static_cast<int>(F - c0 < 128 ? F - c0 : 128);       // multiples of 32
+  const int nrows = static_cast<int>(R - b0 < 128 ? R - b0 : 128);
+  griddep_wait();
+  griddep_launch_dependents();
+
+  {
+    const int q = tid & 15, r1 = tid >> 4;  // rows r1, r1 + 16, ...
+    const bool col_ok = 8 * q < ncols;
+    const __nv_bfloat16 *ph = dh + (b0 + r1) * ld_dh + c0 + 8 * q;
+    const __nv_bfloat16 *pg = gu + (b0 + r1) * ld_gu + c0 + 8 * q;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      uint4 th[2], tg[2], tu[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        th[i] = tg[i] = tu[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (col_ok && r1 + 32 * k + 16 * i < nrows) {
+          th[i] = __ldg(reinterpret_cast<const uint4 *>(ph + i * 16 * ld_dh));
+          tg[i] = __ldg(reinterpret_cast<const uint4 *>(pg + i * 16 * ld_gu));
+          tu[i] = __ldg(reinterpret_cast<const uint4 *>(pg + i * 16 * ld_gu + F));
+        }
+      }
+      ph += 32 * ld_dh;
+      pg += 32 * ld_gu;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t h4[4] = {th[i].x, th[i].y, th[i].z, th[i].w};
+        const uint32_t g4[4] = {tg[i].x, tg[i].y, tg[i].z, tg[i].w};
+        const uint32_t u4[4] = {tu[i].x, tu[i].y, tu[i].z, tu[i].w};
+        uint32_t og[4], ou[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float dg[2], du[2];
+          gate_grad<ACT>(__uint_as_float(h4[j] << 16), __uint_as_float(g4[j] << 16),
+                         __uint_as_float(u4[j] << 16), dg[0], du[0]);
+          gate_grad<ACT>(__uint_as_float(h4[j] & 0xFFFF0000u),
+                         __uint_as_float(g4[j] & 0xFFFF0000u),
+                         __uint_as_float(u4[j] & 0xFFFF0000u), dg[1], du[1]);
+          og[j] = pack_bf16(dg[0], dg[1]);
+          ou[j] = pack_bf16(du[0], du[1]);
+        }
+        const int r = r1 + 32 * k + 16 * i;
+        *reinterpret_cast<uint4 *>(sm + grad_at(r, q)) = make_uint4(og[0], og[1], og[2], og[3]);
+        *reinterpret_cast<uint4 *>(sm + GradSmem::kTile + grad_at(r, q)) =
+            make_uint4(ou[0], ou[1], ou[2], ou[3]);
+        if (d_out && col_ok && r < nrows) {
+          __nv_bfloat16 *d = d_out + (b0 + r) * C + c0 + 8 * q;
+          *reinterpret_cast<uint4 *>(d) = make_uint4(og[0], og[1], og[2], og[3]);
+          *reinterpret_cast<uint4 *>(d + F) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  {  // along the columns of d: 16 columns of rows r1, r1 + 32, ... of both halves
+    const int j = tid & 7, r1 = tid >> 3;
+    uint32_t bad = 0;
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      const int half = k >> 2, r = r1 + 32 * (k & 3);
+      const uint8_t *tile = sm + half * GradSmem::kTile;
+      const uint4 a = *reinterpret_cast<const uint4 *>(tile + grad_at(r, 2 * j));
+      const uint4 b = *reinterpret_cast<const uint4 *>(tile + grad_at(r, 2 * j + 1));
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t mx = bf16_amax_bits(w, bad);
+      mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+      const int e = mx_exponent_e5m2(mx);
+      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      uint32_t codes[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = e5m2x2(__fmul_rn(__uint_as_float(w[2 * i] << 16), inv),
+                                   __fmul_rn(__uint_as_float(w[2 * i] & 0xFFFF0000u), inv));
+        const uint32_t hi = e5m2x2(__fmul_rn(__uint_as_float(w[2 * i + 1] << 16), inv),
+                                   __fmul_rn(__uint_as_float(w[2 * i + 1] & 0xFFFF0000u), inv));
+        codes[i] = __byte_perm(lo, hi, 0x5410);
+      }
+      if (r < nrows && 16 * j < ncols)
+        *reinterpret_cast<uint4 *>(q_row + (b0 + r) * C + half * F + c0 + 16 * j) =
+            make_uint4(codes[0], codes[1], codes[2], codes[3]);
+      if ((j & 1) == 0)
+        sm[GradSmem::kOffSfr + (half * 128 + r) * 4 + (j >> 1)] =
+            static_cast<uint8_t>(r < nrows ? e + 127 : 127);
+    }
+    if (bad && status) atomicOr(status, 1);
+  }
+  // along the rows: columns 2 p, 2 p + 1 of the 32-row group rg of both halves
+  const int p = tid & 63, rg = tid >> 6;
+  uint32_t out[2][2][8];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint8_t *tile = sm + half * GradSmem::kTile + 4 * (p & 3);
+    uint32_t w[32];
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+      w[r] = *reinterpret_cast<const uint32_t *>(tile + grad_at(rg * 32 + r, p >> 2));
+    uint32_t m = 0;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) m = max_u16x2(m, w[r] & 0x7FFF7FFFu);
+    const int e0 = mx_exponent_e5m2(m & 0xFFFFu), e1 = mx_exponent_e5m2(m >> 16);
+    const bool ok = rg * 32 < nrows;
+    uint8_t *sft = sm + GradSmem::kOffSft + (half * 128 + 2 * p) * 4 + rg;
+    sft[0] = static_cast<uint8_t>(ok ? e0 + 127 : 127);
+    sft[4] = static_cast<uint8_t>(ok ? e1 + 127 : 127);
+    const float inv0 = __uint_as_float(static_cast<uint32_t>(127 - e0) << 23);
+    const float inv1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t c[4];  // rows 4 j .. 4 j + 3: column 2 p in the low byte
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        c[t] = e5m2x2(__fmul_rn(__uint_as_float(w[4 * j + t] << 16), inv0),
+                      __fmul_rn(__uint_as_float(w[4 * j + t] & 0xFFFF0000u), inv1));
+      const uint32_t lo = __byte_perm(c[0], c[1], 0x5140), hi = __byte_perm(c[2], c[3], 0x5140);
+      out[half][0][j] = __byte_perm(lo, hi, 0x5410);
+      out[half][1][j] = __byte_perm(lo, hi, 0x7632);
+    }
+  }
+  __syncthreads();  // the tiles have been read
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<uint4 *>(sm + half * 16384 + code_at(2 * p + h, 2 * rg + q)) =
+            make_uint4(out[half][h][4 * q], out[half][h][4 * q + 1], out[half][h][4 * q + 2],
+                       out[half][h][4 * q + 3]);
+  __syncthreads();
+#pragma unroll
+  for (int i = tid; i < 2048; i += 256) {
+    const int half = i >> 10, c = (i >> 3) & 127, q = i & 7;
+    if (c < ncols && 16 * q < nrows)
+      *reinterpret_cast<uint4 *>(q_t + (half * F + c0 + c) * R + b0 + 16 * q) =
+          *reinterpret_cast<const uint4 *>(sm + half * 16384 + code_at(c, q));
+  }
+  const int64_t katoms_t = ((R >> 5) + 3) >> 2, katoms_r = ((C >> 5) + 3) >> 2;
+  {
+    const int half = tid >> 7, t = tid & 127;
+    const int64_t cd = half * F + c0, g = cd >> 5;  // first column and group in d
+    const uint8_t *sfr = sm + GradSmem::kOffSfr + tid * 4;
+    const int ng = ncols >> 5;
+    if (ng == 4 && (g & 3) == 0) {  // a word of a scale atom
+      *reinterpret_cast<uint32_t *>(sf_row + sf_mma_offset(b0 + t, g, katoms_r)) =
+          *reinterpret_cast<const uint32_t *>(sfr);
+    } else {
+      for (int i = 0; i < ng; ++i) sf_row[sf_mma_offset(b0 + t, g + i, katoms_r)] = sfr[i];
+    }
+    if (t < ncols)
+      *reinterpret_cast<uint32_t *>(sf_t + sf_mma_offset(cd + t, b0 >> 5, katoms_t)) =
+          *reinterpret_cast<const uint32_t *>(sm + GradSmem::kOffSft + tid * 4);
+  }
+  if (blockIdx.y == gridDim.y - 1 && tid < 128) {  // padding behind the last column
+    for (int64_t g = C >> 5; g < katoms_r * 4; ++g)
+      sf_row[sf_mma_offset(b0 + tid, g, katoms_r)] = 127;
+    const int64_t c = C + tid;
+    if (c < (C + 127) / 128 * 128)
+      *reinterpret_cast<uint32_t *>(sf_t + sf_mma_offset(c, b0 >> 5, katoms_t)) = 0x7F7F7F7Fu;
   }
 }
 

@@ -36,9 +36,9 @@ struct LinPairSmem {
   static constexpr int kStages = I8 ? 6 : 5;
   static constexpr int kAcc = I8 ? 2 : 1;
   static constexpr int kSfCols = I8 ? 0 : 12;
-  static constexpr int kSlots = 2;  // 128 x 32 bf16 staging tiles, one per epilogue group
+  static constexpr int kSlots = I8 ? 2 : 3;  // 128 x 32 bf16 staging tiles of an epilogue group
   static constexpr int kOffY = kStages * kStageTiles;
-  static constexpr int kOffSf = kOffY + kSlots * kYChunkBytes;
+  static constexpr int kOffSf = kOffY + 2 * kSlots * kYChunkBytes;
   static constexpr int kOffBar = kOffSf + kStages * kSfBytes;
   static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -75,22 +75,34 @@ __device__ __forceinline__ void group_sync(int group) {
   asm volatile("barrier.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
-// One 128-row x 32-column chunk of bf16 outputs (thread = row) through the group's
-// staging tile to the tensor behind `map` at column q0 of rows m0 ...: TMA stores
-// leave out what lies outside the tensor.
-__device__ __forceinline__ void store_chunk(const CUtensorMap *map, uint8_t *slot, int row,
-                                            int group, int group_tid, int q0, int m0, int M,
-                                            int b, const uint32_t (&o)[16]) {
-  if (group_tid == 0) bulk_wait_group_read<0>();  // the group's previous store has read the slot
-  group_sync(group);
+// An epilogue group's way out: its ring of staging tiles and the next one's number.
+template <int SLOTS>
+struct OutRing {
+  uint8_t *base;
+  int row, group, tid;  // tid: 0 .. 127 in the group
+  int next;
+};
+
+// One 128-row x 32-column chunk of bf16 outputs (thread = row) through the ring to
+// the tensor behind `map` at column q0 of rows m0 ...: TMA stores leave out what
+// lies outside the tensor.  A slot is written again once all but the latest
+// SLOTS - 1 stores have read theirs.
+template <int SLOTS>
+__device__ __forceinline__ void store_chunk(OutRing<SLOTS> &ring, const CUtensorMap *map, int q0,
+                                            int m0, int M, int b, const uint32_t (&o)[16]) {
+  uint8_t *slot = ring.base + ring.next * kYChunkBytes;
+  ring.next = ring.next + 1 == SLOTS ? 0 : ring.next + 1;
+  if (ring.tid == 0) bulk_wait_group_read<SLOTS - 1>();
+  group_sync(ring.group);
+  const int row = ring.row;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     *reinterpret_cast<uint4 *>(slot + row * 64 + ((j ^ ((row >> 1) & 3)) << 4)) =
         make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
   fence_proxy_async_smem();
-  group_sync(group);
-  if (group_tid == 0 && m0 < M) {
-    tma_store_3d(map, slot, q0, m0, b);
+  group_sync(ring.group);
+  if (ring.tid == 0) {
+    if (m0 < M) tma_store_3d(map, slot, q0, m0, b);
     bulk_commit_group();
   }
 }
@@ -279,8 +291,8 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
     const int quad = warp % 4;  // TMEM lane quadrant this warp may access
     const int row = quad * 32 + lane;
     const int group = (warp - 4) / 4;
-    const int group_tid = (threadIdx.x - 128) % 128;
-    uint8_t *slot = smem + L::kOffY + group * kYChunkBytes;
+    OutRing<L::kSlots> ring{smem + L::kOffY + group * L::kSlots * kYChunkBytes, row, group,
+                            static_cast<int>(threadIdx.x % 128), 0};
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -323,10 +335,10 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
           if (a.gu) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = pack_bf16(g[2 * j], g[2 * j + 1]);
-            store_chunk(&tm_g, slot, row, group, group_tid, q0, m0, a.M, 0, o);
+            store_chunk(ring, &tm_g, q0, m0, a.M, 0, o);
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = pack_bf16(up[2 * j], up[2 * j + 1]);
-            store_chunk(&tm_u, slot, row, group, group_tid, q0, m0, a.M, 0, o);
+            store_chunk(ring, &tm_u, q0, m0, a.M, 0, o);
           }
           if (a.act == kGateSilu) {
 #pragma unroll
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = pack_bf16(g[2 * j], g[2 * j + 1]);
           if (a.q_out) quant_out_row32(a, 0, m, q0, o);
-          if (a.y) store_chunk(&tm_y, slot, row, group, group_tid, q0, m0, a.M, 0, o);
+          if (a.y) store_chunk(ring, &tm_y, q0, m0, a.M, 0, o);
         }
       } else {
 #pragma unroll 1
@@ -390,7 +402,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
           uint32_t o[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
-          store_chunk(&tm_y, slot, row, group, group_tid, q0, m0, a.M, u.b, o);
+          store_chunk(ring, &tm_y, q0, m0, a.M, u.b, o);
         }
         tc_fence_before();
         __syncwarp();
