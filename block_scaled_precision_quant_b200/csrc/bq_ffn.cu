@@ -10,6 +10,7 @@
 #include "bq.h"
 #include "bq_host.cuh"
 #include "gated_grad.cuh"
+#include "gated_mx.cuh"
 #include "lin_pair.cuh"
 #include "lin_swap.cuh"
 #include "quant_i8.cuh"
@@ -74,7 +75,8 @@ int operand_map(CUtensorMap* m, const void* base, bool fp4, int64_t K, int64_t r
   return r == CUDA_SUCCESS ? BQ_OK : BQ_ERR_ALIGN;
 }
 
-// An MX scale buffer as (128 words, K atoms, 128-row bands), boxes of one atom.
+// An MX scale buffer as (128 words, K atoms, 128-row bands), boxes of kMxSfChunks
+// atoms of a band.
 int scale_map(CUtensorMap* m, const void* base, int64_t rows, int64_t K) {
   auto encode = bqh::tensor_map_encoder();
   if (!encode) return BQ_ERR_CUDA;
@@ -82,7 +84,7 @@ int scale_map(CUtensorMap* m, const void* base, int64_t rows, int64_t K) {
   const cuuint64_t dims[3] = {128u, static_cast<cuuint64_t>(katoms),
                               static_cast<cuuint64_t>(bands)};
   const cuuint64_t strides[2] = {512u, static_cast<cuuint64_t>(katoms * 512)};
-  const cuuint32_t box[3] = {128u, 1u, 1u};
+  const cuuint32_t box[3] = {128u, bq::kMxSfChunks, 1u};
   const cuuint32_t step[3] = {1u, 1u, 1u};
   const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims,
                             strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -175,7 +177,9 @@ int make_plan(Kind kind, bool gated, int64_t M, int64_t N, int64_t K, int64_t ba
   const bool pair_asked = c.swap_ab == 0 || c.cta_pair == 2 || c.block_n == 256;
   const bool swap_asked = !pair_asked && (c.swap_ab == 1 || c.cta_pair == 1 || c.split_k > 0 ||
                                           c.block_n != 0);
-  const int64_t pair_p = ceil_div(M, 256), pair_q = ceil_div(N, gated ? 128 : 256);
+  // outputs of a pair's tile (lin_pair.cuh, gated_mx.cuh)
+  const int pair_n = gated ? 128 : 256;
+  const int64_t pair_p = ceil_div(M, 256), pair_q = ceil_div(N, pair_n);
   const int64_t tiles_p = ceil_div(N, 128);
   double best = 1e30;
   for (int bn = 32; bn <= 128 && !pair_asked; bn *= 2) {
@@ -230,24 +234,18 @@ int launch_swap(const Plan& pl, const CUtensorMap& w0, const CUtensorMap& w1,
                 L::kBytes, pl.splits, stream, w0, w1, ta, a);
 }
 
-using Map = CUtensorMap;
-
-template <bool I8, bool GATED>
-int launch_pair(const Plan& pl, const Map& ta, const Map& w0, const Map& w1, const Map& sfa,
-                const Map& sf0, const Map& sf1, const Map& ty, const Map& tg, const Map& tu,
-                const bq::FfnArgs& a, const Device& dev, bq_stream_t stream) {
-  using L = bq::LinPairSmem<I8>;
-  auto kern = bq::lin_pair_kernel<I8, GATED>;
-  static bool ready[bqh::kMaxDevices] = {};
+// A kernel on pairs of SMs: persistent, one pair to every two SMs.
+template <class... P, class... A>
+int launch_pairs(void (*kern)(P...), bool* ready, int threads, int smem, const Plan& pl,
+                 const Device& dev, bq_stream_t stream, const A&... args) {
   if (!ready[dev.index]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
       return BQ_ERR_CUDA;
     ready[dev.index] = true;
   }
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(dev.num_sms / 2, pl.tiles));
-  return launch(kern, dim3(static_cast<unsigned>(2 * pairs)), bq::kLinPairThreads, L::kBytes, 2,
-                stream, ta, w0, w1, sfa, sf0, sf1, ty, tg, tu, a);
+  return launch(kern, dim3(static_cast<unsigned>(2 * pairs)), threads, smem, 2, stream, args...);
 }
 
 template <bool I8, bool GATED>
@@ -355,30 +353,33 @@ int run(const Call& c, bool gated, bool empty, const bq_gemm_config* cfg, bq::Ff
   if (pl.pair) {
     g->raster_group = 4;
     g->splits = 1;
+    const bool mx = !i8;
     st = operand_map(&ta, c.a, false, c.K, c.M, g->q_batched ? c.batch.count : 1,
                      c.batch.stride_a, 128);
     for (int w = 0; st == BQ_OK && w < (gated ? 2 : 1); ++w)
       st = operand_map(&tw[w], c.w[w], fp4, c.K, c.N, g->p_batched ? c.batch.count : 1,
                        c.batch.stride_b, 128);
     if (st != BQ_OK) return st;
-    CUtensorMap sfa = ta, sf[2] = {ta, ta}, ty = ta, tg = ta, tu = ta;  // unused: placeholders
-    if (!i8) {
-      st = scale_map(&sfa, c.a_sf, c.M, c.K);
-      for (int w = 0; st == BQ_OK && w < 2; ++w) st = scale_map(&sf[w], c.w_sf[w], c.N, c.K);
-    }
-    if (st == BQ_OK && g->y)
-      st = output_map(&ty, g->y, c.M, c.N, c.N, c.batch.count, c.batch.stride_y);
+    CUtensorMap ty = ta, tg = ta, tu = ta;  // unused ones: placeholders
+    if (g->y) st = output_map(&ty, g->y, c.M, c.N, c.N, c.batch.count, c.batch.stride_y);
     if (st == BQ_OK && g->gu) st = output_map(&tg, g->gu, c.M, c.N, 2 * c.N, 1, 0);
     if (st == BQ_OK && g->gu) st = output_map(&tu, g->gu + c.N, c.M, c.N, 2 * c.N, 1, 0);
     if (st != BQ_OK) return st;
-    const bq_stream_t s = stream;
-    if (!gated)
-      return launch_pair<true, false>(pl, ta, tw[0], tw[0], sfa, sf[0], sf[1], ty, tg, tu, *g, dev,
-                                      s);
-    return i8 ? launch_pair<true, true>(pl, ta, tw[0], tw[1], sfa, sf[0], sf[1], ty, tg, tu, *g,
-                                        dev, s)
-              : launch_pair<false, true>(pl, ta, tw[0], tw[1], sfa, sf[0], sf[1], ty, tg, tu, *g,
-                                         dev, s);
+    static bool ready[3][bqh::kMaxDevices] = {};
+    if (mx) {
+      CUtensorMap sfa, sf[2];
+      st = scale_map(&sfa, c.a_sf, c.M, c.K);
+      for (int w = 0; st == BQ_OK && w < 2; ++w) st = scale_map(&sf[w], c.w_sf[w], c.N, c.K);
+      if (st != BQ_OK) return st;
+      return launch_pairs(bq::gated_mx_kernel, ready[0], bq::kMxThreads, bq::GatedMxSmem::kBytes,
+                          pl, dev, stream, ta, tw[0], tw[1], sfa, sf[0], sf[1], ty, tg, tu, *g);
+    }
+    return gated ? launch_pairs(bq::lin_pair_kernel<true>, ready[1], bq::kLinPairThreads,
+                                bq::LinPairSmem::kBytes, pl, dev, stream, ta, tw[0], tw[1], ty, tg,
+                                tu, *g)
+                 : launch_pairs(bq::lin_pair_kernel<false>, ready[2], bq::kLinPairThreads,
+                                bq::LinPairSmem::kBytes, pl, dev, stream, ta, tw[0], tw[0], ty, tg,
+                                tu, *g);
   }
   // One tile over all rows: its box ends at the last row (a box whose trailing
   // rows all lie outside the tensor copies slower).

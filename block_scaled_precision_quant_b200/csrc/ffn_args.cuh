@@ -52,15 +52,45 @@ __host__ __device__ constexpr uint32_t idesc_i8(int m, int n) {
          | (static_cast<uint32_t>(m >> 4) << 24); // M / 16
 }
 
-// g / (1 + e^-g) with the fast exponential and division (relative errors near
-// 2^-21, half a bf16 step is 2^-9).  e^-g overflows to +inf for g < -88, where
-// the quotient's -0 is the value's own rounding.
+__device__ __forceinline__ float rcp_fast(float x) {  // relative error 2^-23
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {  // relative error 2^-22
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// g / (1 + e^-g): relative error near 2^-20 (half a bf16 step is 2^-8).  Below
+// g = -87 the quotient, under 2^-118, comes out as -0.
 __device__ __forceinline__ float silu(float g) {
-  return __fdividef(g, 1.0f + __expf(-g));
+  return g * rcp_fast(1.0f + exp2_fast(-kLog2e * g));
+}
+
+// e^(-g^2 / 2), and P(g) = (1 + erf(g / sqrt 2)) / 2 by the formula of gelu_erf
+// (Abramowitz and Stegun 7.1.26, absolute error 0.8e-7).
+__device__ __forceinline__ float gelu_cdf(float g, float &e) {
+  const float x = fabsf(g) * 0.70710678118654752f;
+  const float k = rcp_fast(fmaf(0.3275911f, x, 1.0f));
+  float poly = fmaf(k, 1.061405429f, -1.453152027f);
+  poly = fmaf(k, poly, 1.421413741f);
+  poly = fmaf(k, poly, -0.284496736f);
+  poly = fmaf(k, poly, 0.254829592f);
+  e = exp2_fast(-kLog2e * x * x);
+  const float half_erfc = 0.5f * k * poly * e;  // of |g| / sqrt 2
+  return g >= 0.0f ? 1.0f - half_erfc : half_erfc;
+}
+
+__device__ __forceinline__ float gelu_gate(float g) {
+  float e;
+  return g * gelu_cdf(g, e);
 }
 
 __device__ __forceinline__ float gate_act(float g, int act) {
-  return act == kGateSilu ? silu(g) : gelu_erf(g);
+  return act == kGateSilu ? silu(g) : gelu_gate(g);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

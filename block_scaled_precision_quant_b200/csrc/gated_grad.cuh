@@ -21,19 +21,12 @@ namespace bq {
 template <int ACT>
 __device__ __forceinline__ void gate_grad(float dh, float g, float u, float &dg, float &du) {
   if constexpr (ACT == kGateSilu) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-g));
-    du = dh * (g * s);
-    dg = dh * u * (s * fmaf(g, 1.0f - s, 1.0f));
+    const float s = rcp_fast(1.0f + exp2_fast(-kLog2e * g)), t = g * s;
+    du = dh * t;
+    dg = dh * u * fmaf(t, 1.0f - s, s);  // act' = s (1 + g (1 - s))
   } else {
-    const float x = fabsf(g) * 0.70710678118654752f;
-    const float k = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    float poly = fmaf(k, 1.061405429f, -1.453152027f);
-    poly = fmaf(k, poly, 1.421413741f);
-    poly = fmaf(k, poly, -0.284496736f);
-    poly = fmaf(k, poly, 0.254829592f);
-    const float e = __expf(-x * x);  // e^(-g^2 / 2)
-    const float erfc_x = k * poly * e;
-    const float p = 0.5f * (g >= 0.0f ? 2.0f - erfc_x : erfc_x);
+    float e;
+    const float p = gelu_cdf(g, e);
     du = dh * (g * p);
     dg = dh * u * fmaf(0.39894228040143268f * g, e, p);
   }

@@ -1,6 +1,6 @@
 // lin_pair.cuh -- int8 products and gated feed-forward blocks with many rows:
 // 256-row tiles on pairs of SMs (a cluster of 2), computed by tcgen05 MMAs of
-// the cta_group::2 form with M = 256, N = 256.
+// the cta_group::2 form with M = 256, N = 256.  (MX operands: gated_mx.cuh.)
 //
 // A pair's tile is 256 rows of A against 256 weight rows.  Each CTA loads its
 // own 128 rows of A and 128 of the weight rows; the pair's MMAs, issued by the
@@ -12,10 +12,8 @@
 // product is formed in the registers of one thread.
 //
 // Per 128 K an SM brings 32 KB into shared memory for 512 cycles of MMAs, a
-// third less than a 128 x 256 tile of its own needs.  Int8 keeps two sets of
-// sums (2 x 256 TMEM columns): the epilogue of one tile runs under the MMAs of
-// the next.  MX tiles need TMEM for scales and keep one set, which the
-// epilogue reads into registers and gives back before it goes on.
+// third less than a 128 x 256 tile of its own needs.  Two sets of sums (2 x 256
+// TMEM columns): the epilogue of one tile runs under the MMAs of the next.
 #pragma once
 
 #include "ffn_args.cuh"
@@ -23,28 +21,23 @@
 
 namespace bq {
 
-// Warps: 0 activation tile copies, 1 TMEM and MMA issue, 2 weight tile copies,
-// 3 scale copies (MX), 4-7 and 8-11 two epilogue groups.
-constexpr int kLinPairThreads = 384;
+// Warps: 0 activation tile copies, 1 TMEM and MMA issue, 2 weight tile copies, 3
+// none, 4-19 four epilogue groups of four, one warp to a quadrant of the TMEM
+// lanes.
+constexpr int kLinPairThreads = 640;
+constexpr int kPairGroups = 4;
 
-template <bool I8>
 struct LinPairSmem {
   static constexpr int kBytesA = kBlockP * kBlockK;  // this CTA's 128 rows of A
   static constexpr int kBytesB = kBlockP * kBlockK;  // its 128 weight rows
   static constexpr int kStageTiles = kBytesA + kBytesB;
-  static constexpr int kSfBytes = I8 ? 0 : 3 * kSfAtom;  // A's band, both weight bands
-  static constexpr int kStages = I8 ? 6 : 5;
-  static constexpr int kAcc = I8 ? 2 : 1;
-  static constexpr int kSfCols = I8 ? 0 : 12;
-  static constexpr int kSlots = I8 ? 2 : 3;  // 128 x 32 bf16 staging tiles of an epilogue group
-  static constexpr int kOffY = kStages * kStageTiles;
-  static constexpr int kOffSf = kOffY + 2 * kSlots * kYChunkBytes;
-  static constexpr int kOffBar = kOffSf + kStages * kSfBytes;
-  static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 1;
+  static constexpr int kStages = 6;
+  static constexpr int kOffY = kStages * kStageTiles;  // a 128 x 32 bf16 staging tile a group
+  static constexpr int kOffBar = kOffY + kPairGroups * kYChunkBytes;
+  static constexpr int kNumBars = 2 * kStages + 2 * 2 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 64 + 1024;  // + alignment slack
   static constexpr int kTmemCols = 512;
-  static_assert(kAcc * 256 + kStages * kSfCols <= kTmemCols, "TMEM budget");
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -75,72 +68,99 @@ __device__ __forceinline__ void group_sync(int group) {
   asm volatile("barrier.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
-// An epilogue group's way out: its ring of staging tiles and the next one's number.
-template <int SLOTS>
-struct OutRing {
-  uint8_t *base;
+// An epilogue group's way out: its staging tile.
+struct OutSlot {
+  uint8_t *slot;
   int row, group, tid;  // tid: 0 .. 127 in the group
-  int next;
 };
 
-// One 128-row x 32-column chunk of bf16 outputs (thread = row) through the ring to
-// the tensor behind `map` at column q0 of rows m0 ...: TMA stores leave out what
-// lies outside the tensor.  A slot is written again once all but the latest
-// SLOTS - 1 stores have read theirs.
-template <int SLOTS>
-__device__ __forceinline__ void store_chunk(OutRing<SLOTS> &ring, const CUtensorMap *map, int q0,
+// One 128-row x 32-column chunk of bf16 outputs (thread = row) through the group's
+// staging tile to the tensor behind `map` at column q0 of rows m0 ...: TMA stores
+// leave out what lies outside the tensor.
+__device__ __forceinline__ void store_chunk(const OutSlot &out, const CUtensorMap *map, int q0,
                                             int m0, int M, int b, const uint32_t (&o)[16]) {
-  uint8_t *slot = ring.base + ring.next * kYChunkBytes;
-  ring.next = ring.next + 1 == SLOTS ? 0 : ring.next + 1;
-  if (ring.tid == 0) bulk_wait_group_read<SLOTS - 1>();
-  group_sync(ring.group);
-  const int row = ring.row;
+  if (out.tid == 0) bulk_wait_group_read<0>();  // the group's previous store has read the tile
+  group_sync(out.group);
+  const int row = out.row;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4 *>(slot + row * 64 + ((j ^ ((row >> 1) & 3)) << 4)) =
+    *reinterpret_cast<uint4 *>(out.slot + row * 64 + ((j ^ ((row >> 1) & 3)) << 4)) =
         make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
   fence_proxy_async_smem();
-  group_sync(ring.group);
-  if (ring.tid == 0) {
-    if (m0 < M) tma_store_3d(map, slot, q0, m0, b);
+  group_sync(out.group);
+  if (out.tid == 0 && m0 < M) {
+    tma_store_3d(map, out.slot, q0, m0, b);
     bulk_commit_group();
   }
 }
 
-// The fp32 values alpha * scale * sum of 32 columns n ... of one row.  Int8: `sa`
-// is the row's scale, sw the columns' (n % 8 == 0 keeps each read of four inside).
-template <bool I8>
+// The fp32 values alpha sa sw[n] sum of 32 columns n ... of one row (n % 8 == 0
+// keeps each read of four scales inside).
 __device__ __forceinline__ void scaled32(const uint32_t (&v)[32], float alpha, float sa,
                                          const float *sw, int n, int N, float (&f)[32]) {
-  if constexpr (I8) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (n + 4 * j < N) s = __ldg(reinterpret_cast<const float4 *>(sw + n) + j);
-      const float s4[4] = {s.x, s.y, s.z, s.w};
+  for (int j = 0; j < 8; ++j) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n + 4 * j < N) s = __ldg(reinterpret_cast<const float4 *>(sw + n) + j);
+    const float s4[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        f[4 * j + i] = __int2float_rn(static_cast<int>(v[4 * j + i])) * (sa * (alpha * s4[i]));
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) f[j] = alpha * __uint_as_float(v[j]);
+    for (int i = 0; i < 4; ++i)
+      f[4 * j + i] = __int2float_rn(static_cast<int>(v[4 * j + i])) * (sa * (alpha * s4[i]));
   }
 }
 
-template <bool I8, bool GATED>
+// 32 gated outputs of one row (columns q0 ...), from g and u: the projections on
+// request, h = act(g) u, its codes and scales on request.
+__device__ __forceinline__ void gated_out(const FfnArgs &a, const OutSlot &out,
+                                          const CUtensorMap *tm_y, const CUtensorMap *tm_g,
+                                          const CUtensorMap *tm_u, float (&g)[32],
+                                          const float (&up)[32], int q0, int m0) {
+  uint32_t o[16];
+  if (a.gu) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] = pack_bf16(g[2 * j], g[2 * j + 1]);
+    store_chunk(out, tm_g, q0, m0, a.M, 0, o);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] = pack_bf16(up[2 * j], up[2 * j + 1]);
+    store_chunk(out, tm_u, q0, m0, a.M, 0, o);
+  }
+  if (a.act == kGateSilu) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) g[j] = silu(g[j]) * up[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) g[j] = gelu_gate(g[j]) * up[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) o[j] = pack_bf16(g[2 * j], g[2 * j + 1]);
+  if (a.q_out) quant_out_row32(a, 0, m0 + out.row, q0, o);
+  if (a.y) store_chunk(out, tm_y, q0, m0, a.M, 0, o);
+}
+
+// The same from fp32 sums (their bits).
+__device__ __forceinline__ void gated_chunk(const FfnArgs &a, const OutSlot &out,
+                                            const CUtensorMap *tm_y, const CUtensorMap *tm_g,
+                                            const CUtensorMap *tm_u, const uint32_t (&vg)[32],
+                                            const uint32_t (&vu)[32], int q0, int m0) {
+  float g[32], up[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    g[j] = a.alpha * __uint_as_float(vg[j]);
+    up[j] = a.alpha * __uint_as_float(vu[j]);
+  }
+  gated_out(a, out, tm_y, tm_g, tm_u, g, up, q0, m0);
+}
+
+template <bool GATED>
 __global__ void __launch_bounds__(kLinPairThreads, 1)
     lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                     const __grid_constant__ CUtensorMap tm_w0,
                     const __grid_constant__ CUtensorMap tm_w1,
-                    const __grid_constant__ CUtensorMap tm_sfa,
-                    const __grid_constant__ CUtensorMap tm_sf0,
-                    const __grid_constant__ CUtensorMap tm_sf1,
                     const __grid_constant__ CUtensorMap tm_y,
                     const __grid_constant__ CUtensorMap tm_g,
                     const __grid_constant__ CUtensorMap tm_u, const FfnArgs a) {
-  using L = LinPairSmem<I8>;
-  constexpr int kStages = L::kStages, kAcc = L::kAcc;
+  using L = LinPairSmem;
+  constexpr int kStages = L::kStages, kAcc = 2;
   constexpr int kTileN = GATED ? 128 : 256;  // outputs of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -161,23 +181,18 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int st = 0; st < kStages; ++st) {
-      mbar_init(&full[st], I8 ? 2 : 3);  // the leader's copy threads (bytes of both CTAs)
-      mbar_init(&empty[st], 1);          // the leader's commit
+      mbar_init(&full[st], 2);   // the leader's copy threads (bytes of both CTAs)
+      mbar_init(&empty[st], 1);  // the leader's commit
     }
     for (int i = 0; i < kAcc; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 16);  // every epilogue warp of both CTAs
+      mbar_init(&tempty[i], 8 * kPairGroups);  // every epilogue warp of both CTAs
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(rank == 1 && GATED ? &tm_w1 : &tm_w0);
-    if (!I8) {
-      tma_prefetch_desc(&tm_sfa);
-      tma_prefetch_desc(&tm_sf0);
-      tma_prefetch_desc(&tm_sf1);
-    }
   }
   if (warp == 1) tmem_alloc2(tmem_slot, L::kTmemCols);
   tc_fence_before();
@@ -188,43 +203,32 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp == 0 || warp == 2 || (!I8 && warp == 3)) {
-    // ------------------------------------------------------------- copies --
+  if (warp == 0 || warp == 2) {
+    // -------------------------------------------------------- tile copies --
     if (lane == 0) {
-      if (warp != 2) {  // activations and their scales may come from the kernel before
+      if (warp == 0) {  // the activations may come from the kernel before
         griddep_wait();
-        if (warp == 0) griddep_launch_dependents();
+        griddep_launch_dependents();
       }
-      const uint32_t tx = warp == 0   ? 2 * L::kBytesA
-                          : warp == 2 ? 2 * a.w_tile_bytes
-                                      : 2 * static_cast<uint32_t>(L::kSfBytes);
+      const uint32_t tx = warp == 0 ? 2 * L::kBytesA : 2 * a.w_tile_bytes;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int unit = pair; unit < total_units && ok; unit += num_pairs) {
         const UnitPos u = unit_pos(a, unit);
-        const int band = 2 * u.tp + static_cast<int>(rank);  // this CTA's 128 rows of A
-        const int brow = GATED ? u.tq * 128 : u.tq * 256 + static_cast<int>(rank) * 128;
-        const int ba = a.q_batched ? u.b : 0, bw = a.p_batched ? u.b : 0;
+        const int row = warp == 0 ? (2 * u.tp + static_cast<int>(rank)) * 128
+                        : GATED   ? u.tq * 128
+                                  : u.tq * 256 + static_cast<int>(rank) * 128;
+        const int bt = warp == 0 ? (a.q_batched ? u.b : 0) : (a.p_batched ? u.b : 0);
+        const CUtensorMap *map = warp == 0 ? &tm_a : GATED && rank == 1 ? &tm_w1 : &tm_w0;
         for (int kt = 0; kt < a.kt_total; ++kt) {
           if (!mbar_wait(&empty[stage], phase ^ 1, a.err, abort_flag, kWaitProdEmpty)) {
             ok = false;
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], tx);
-          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-          uint8_t *tiles = smem + stage * L::kStageTiles;
-          if (warp == 0) {
-            tma2_load_3d(tiles, &tm_a, bar, kt * kBlockK, band * 128, ba);
-          } else if (warp == 2) {
-            tma2_load_3d(tiles + L::kBytesA, GATED && rank == 1 ? &tm_w1 : &tm_w0, bar,
-                         kt * kBlockK, brow, bw);
-          } else {
-            uint8_t *sf = smem + L::kOffSf + stage * L::kSfBytes;
-            tma2_load_3d(sf, &tm_sfa, bar, 0, kt, band);
-            tma2_load_3d(sf + kSfAtom, &tm_sf0, bar, 0, kt, u.tq);
-            tma2_load_3d(sf + 2 * kSfAtom, &tm_sf1, bar, 0, kt, u.tq);
-          }
+          tma2_load_3d(smem + stage * L::kStageTiles + (warp == 0 ? 0 : L::kBytesA), map,
+                       mapa_shared(smem_u32(&full[stage]), 0), kt * kBlockK, row, bt);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------- MMA issue (leader) --
     if (rank == 0 && lane == 0) {
-      const uint32_t tiles0 = smem_u32(smem), sf0 = smem_u32(smem + L::kOffSf);
+      const uint32_t tiles0 = smem_u32(smem);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -252,24 +256,10 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
           }
           tc_fence_after();
           const uint32_t ta = tiles0 + stage * L::kStageTiles, tb = ta + L::kBytesA;
-          const uint32_t sf_t = tmem_base + kAcc * 256 + stage * L::kSfCols;
-          if constexpr (!I8) {
 #pragma unroll
-            for (int j = 0; j < 3; ++j)
-              tc_cp_sf2(sf_t + 4 * j,
-                        desc_sf_32x128b(sf0 + stage * L::kSfBytes + j * kSfAtom));
-          }
-#pragma unroll
-          for (int ks = 0; ks < kBlockK / kMmaK; ++ks) {
-            const uint32_t acc_in = (kt > 0 || ks > 0) ? 1u : 0u;
-            const uint64_t da = desc_kmajor_sw128(ta + ks * kMmaK);
-            const uint64_t db = desc_kmajor_sw128(tb + ks * kMmaK);
-            if constexpr (I8)
-              tc_mma2_i8(d, da, db, idesc_i8(256, 256), acc_in);
-            else
-              tc_mma2_mxf8f6f4(d, da, db, make_idesc_m(a.fmt_a, a.fmt_w, 256, 256, ks), sf_t,
-                               sf_t + 4, acc_in);
-          }
+          for (int ks = 0; ks < kBlockK / kMmaK; ++ks)
+            tc_mma2_i8(d, desc_kmajor_sw128(ta + ks * kMmaK), desc_kmajor_sw128(tb + ks * kMmaK),
+                       idesc_i8(256, 256), (kt > 0 || ks > 0) ? 1u : 0u);
           tc_commit2_both(&empty[stage]);
           if (++stage == kStages) {
             stage = 0;
@@ -291,8 +281,8 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
     const int quad = warp % 4;  // TMEM lane quadrant this warp may access
     const int row = quad * 32 + lane;
     const int group = (warp - 4) / 4;
-    OutRing<L::kSlots> ring{smem + L::kOffY + group * L::kSlots * kYChunkBytes, row, group,
-                            static_cast<int>(threadIdx.x % 128), 0};
+    const OutSlot out{smem + L::kOffY + group * kYChunkBytes, row, group,
+                      static_cast<int>(threadIdx.x % 128)};
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -302,59 +292,32 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
       const int m0 = (2 * u.tp + static_cast<int>(rank)) * 128, m = m0 + row;
       const int n0 = u.tq * kTileN;
       const bool mok = m < a.M;
-      const float sa = I8 && mok ? __ldg(a.sa + u.b * a.sa_bstride + m) : 0.0f;
+      const float sa = mok ? __ldg(a.sa + u.b * a.sa_bstride + m) : 0.0f;
       __syncwarp();
       if (!mbar_wait_cluster(&tfull[acc], acc_phase, a.err, abort_flag, kWaitEpiFull)) break;
       tc_fence_after();
       const uint32_t t_row = tmem_base + acc * 256 + (static_cast<uint32_t>(quad * 32) << 16);
       const int nch = min(kTileN / 32, (a.N - n0 + 31) / 32);
       if constexpr (GATED) {
-        // This group's two chunks of 32 outputs: first all sums into registers,
-        // then the sums' TMEM goes back to the MMAs.
-        uint32_t vg[2][32], vu[2][32];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = group + 2 * i;
-          __syncwarp();
-          tmem_ld_32x32b_x32(t_row + c * 32, vg[i]);
-          tmem_ld_32x32b_x32(t_row + 128 + c * 32, vu[i]);
-        }
+        // This group's 32 outputs: all sums into registers, then their TMEM goes
+        // back to the MMAs.
+        const int q0 = n0 + group * 32;
+        uint32_t vg[32], vu[32];
+        tmem_ld_32x32b_x32(t_row + group * 32, vg);
+        tmem_ld_32x32b_x32(t_row + 128 + group * 32, vu);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(lead_tempty + acc * 8);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = group + 2 * i;
-          if (c >= nch) break;  // uniform
-          const int q0 = n0 + c * 32;
+        if (group < nch) {  // uniform
           float g[32], up[32];
-          scaled32<I8>(vg[i], a.alpha, sa, a.sw[0], q0, a.N, g);
-          scaled32<I8>(vu[i], a.alpha, sa, a.sw[1], q0, a.N, up);
-          uint32_t o[16];
-          if (a.gu) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = pack_bf16(g[2 * j], g[2 * j + 1]);
-            store_chunk(ring, &tm_g, q0, m0, a.M, 0, o);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = pack_bf16(up[2 * j], up[2 * j + 1]);
-            store_chunk(ring, &tm_u, q0, m0, a.M, 0, o);
-          }
-          if (a.act == kGateSilu) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) g[j] = silu(g[j]) * up[j];
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) g[j] = gelu_erf(g[j]) * up[j];
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = pack_bf16(g[2 * j], g[2 * j + 1]);
-          if (a.q_out) quant_out_row32(a, 0, m, q0, o);
-          if (a.y) store_chunk(ring, &tm_y, q0, m0, a.M, 0, o);
+          scaled32(vg, a.alpha, sa, a.sw[0], q0, a.N, g);
+          scaled32(vu, a.alpha, sa, a.sw[1], q0, a.N, up);
+          gated_out(a, out, &tm_y, &tm_g, &tm_u, g, up, q0, m0);
         }
       } else {
 #pragma unroll 1
-        for (int c = group; c < nch; c += 2) {
+        for (int c = group; c < nch; c += kPairGroups) {
           const int q0 = n0 + c * 32;
           uint32_t v[32];
           __syncwarp();
@@ -370,7 +333,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
           }
           tmem_ld_wait();
           float f[32];
-          scaled32<I8>(v, a.alpha, sa, a.sw[0] + u.b * a.sw_bstride, q0, a.N, f);
+          scaled32(v, a.alpha, sa, a.sw[0] + u.b * a.sw_bstride, q0, a.N, f);
           if (a.bias) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -402,7 +365,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
           uint32_t o[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
-          store_chunk(ring, &tm_y, q0, m0, a.M, u.b, o);
+          store_chunk(out, &tm_y, q0, m0, a.M, u.b, o);
         }
         tc_fence_before();
         __syncwarp();
@@ -417,7 +380,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
 
   // The last stores are done, and neither CTA's barriers, shared memory or TMEM
   // are in use, when the pair leaves.
-  if (threadIdx.x == 128 || threadIdx.x == 256) bulk_wait_group_all();
+  if (threadIdx.x >= 128 && threadIdx.x % 128 == 0) bulk_wait_group_all();
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
