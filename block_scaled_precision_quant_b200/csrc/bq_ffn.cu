@@ -143,23 +143,23 @@ int check_config(const bq_gemm_config* cfg) {
   return BQ_OK;
 }
 
-// Estimated microseconds of the two schedules, fitted to sweeps over 1 to 2048
-// rows, 512 to 16384 outputs and K of 512 to 8192 (within about 15 % of them).
-// What either spends its time on is filling shared memory, about 105 KB a
-// microsecond and SM, so a tile's cost is the bytes of its K blocks.
-//   swap: launch, first copies and outputs 3.8 us, longer by the tile's rows;
-//         a split adds the exchange (int8 41 x 4608 x 1536: 6.4 us unsplit, 6.1 in
-//         4 slices; 41 x 1536 x 6144: 14.5 and 6.7 in 8; gated 41 x 6144 x 1536:
-//         10.4 and 8.6 in 2, 9.3 in 4).
+// Estimated microseconds of the two schedules, fitted to sweeps over 1 to 2750
+// rows, 376 to 16384 outputs and K of 304 to 9008 (most within 15 %).
+//   swap: launch, first copies and outputs 3.8 us, longer by the tile's rows.  A CTA
+//         fills its shared memory at about 105 KB/us, all of them at 12 GB/ms from
+//         L2.  A split adds the exchange (int8 41 x 4608 x 1536: 6.4 us unsplit, 6.1
+//         in 4 slices; 41 x 1536 x 6144: 14.5 and 6.7 in 8; gated 41 x 6144 x 1536:
+//         10.4 and 8.6 in 2, 9.3 in 4), more CTAs than SMs their start (int8 795 x
+//         4176 x 304: 11.0 in 64-row tiles, 8.5 in 128-row ones, 7.7 in pairs).
 //   pair: 6.3 us (gated 7.5) and 0.29 us a K block of 256 x 256 (int8 256 x 4096 x
 //         4096: 15.6 us, 12.0 as 64-row tiles; 1024 x 4096 x 4096: 17.8, 28 as
 //         128-row tiles; 512 x 1024 x 1024: 8.4, 5.6 as 64-row tiles).
 double swap_us(int bn, int64_t tiles, int splits, int kt, bool gated, int num_sms) {
   const double ctas = static_cast<double>(tiles * splits);
-  const double share =  // CTAs that share an SM's bandwidth
-      ctas <= 2.0 * num_sms ? (ctas <= num_sms ? 1.0 : 2.0) : ctas / num_sms;
-  const double chunk_kb = (gated ? 32 : 16) + bn / 8.0;
-  return 3.8 + bn / 128.0 * 0.8 * (gated ? 2 : 1) + share * kt / splits * chunk_kb / 105.0 +
+  const double kb = static_cast<double>(kt) / splits * ((gated ? 32 : 16) + bn / 8.0);  // a CTA's
+  const double starts =
+      ctas <= num_sms ? 0.0 : 1.5 + 3.5 * static_cast<double>((tiles * splits - 1) / (2 * num_sms));
+  return 3.8 + bn / 128.0 * 0.8 * (gated ? 2 : 1) + starts + std::max(kb / 105, ctas * kb / 12e3) +
          (splits > 1 ? bn / 64.0 * 1.6 : 0.0);
 }
 
@@ -365,7 +365,7 @@ int run(const Call& c, bool gated, bool empty, const bq_gemm_config* cfg, bq::Ff
     if (st == BQ_OK && g->gu) st = output_map(&tg, g->gu, c.M, c.N, 2 * c.N, 1, 0);
     if (st == BQ_OK && g->gu) st = output_map(&tu, g->gu + c.N, c.M, c.N, 2 * c.N, 1, 0);
     if (st != BQ_OK) return st;
-    static bool ready[3][bqh::kMaxDevices] = {};
+    static bool ready[4][bqh::kMaxDevices] = {};
     if (mx) {
       CUtensorMap sfa, sf[2];
       st = scale_map(&sfa, c.a_sf, c.M, c.K);
@@ -374,12 +374,23 @@ int run(const Call& c, bool gated, bool empty, const bq_gemm_config* cfg, bq::Ff
       return launch_pairs(bq::gated_mx_kernel, ready[0], bq::kMxThreads, bq::GatedMxSmem::kBytes,
                           pl, dev, stream, ta, tw[0], tw[1], sfa, sf[0], sf[1], ty, tg, tu, *g);
     }
-    return gated ? launch_pairs(bq::lin_pair_kernel<true>, ready[1], bq::kLinPairThreads,
-                                bq::LinPairSmem::kBytes, pl, dev, stream, ta, tw[0], tw[1], ty, tg,
-                                tu, *g)
-                 : launch_pairs(bq::lin_pair_kernel<false>, ready[2], bq::kLinPairThreads,
-                                bq::LinPairSmem::kBytes, pl, dev, stream, ta, tw[0], tw[0], ty, tg,
-                                tu, *g);
+    constexpr int kT = bq::kLinPairThreads;
+    if (gated)
+      return launch_pairs(bq::lin_pair_kernel<true, false>, ready[1], kT,
+                          bq::LinPairSmem<false>::kBytes, pl, dev, stream, ta, tw[0], tw[1], ty, tg,
+                          tu, *g);
+    if (!g->res)
+      return launch_pairs(bq::lin_pair_kernel<false, false>, ready[2], kT,
+                          bq::LinPairSmem<false>::kBytes, pl, dev, stream, ta, tw[0], tw[0], ty, tg,
+                          tu, *g);
+    CUtensorMap tr;  // one residual for every problem: no batch dimension
+    if (c.batch.count <= 1) g->res_bstride = 0;
+    st = output_map(&tr, g->res, c.M, c.N, g->ldres, g->res_bstride ? c.batch.count : 1,
+                    c.batch.stride_res);
+    if (st != BQ_OK) return st;
+    return launch_pairs(bq::lin_pair_kernel<false, true>, ready[3], kT,
+                        bq::LinPairSmem<true>::kBytes, pl, dev, stream, ta, tw[0], tw[0], ty, tr, tu,
+                        *g);
   }
   // One tile over all rows: its box ends at the last row (a box whose trailing
   // rows all lie outside the tensor copies slower).

@@ -27,14 +27,18 @@ namespace bq {
 constexpr int kLinPairThreads = 640;
 constexpr int kPairGroups = 4;
 
+// RES: products with a residual, whose chunks come by TMA into the staging tiles
+// before the sums stand; two tiles a group then, for one operand stage less.
+template <bool RES>
 struct LinPairSmem {
   static constexpr int kBytesA = kBlockP * kBlockK;  // this CTA's 128 rows of A
   static constexpr int kBytesB = kBlockP * kBlockK;  // its 128 weight rows
   static constexpr int kStageTiles = kBytesA + kBytesB;
-  static constexpr int kStages = 6;
-  static constexpr int kOffY = kStages * kStageTiles;  // a 128 x 32 bf16 staging tile a group
-  static constexpr int kOffBar = kOffY + kPairGroups * kYChunkBytes;
-  static constexpr int kNumBars = 2 * kStages + 2 * 2 + 1;
+  static constexpr int kStages = RES ? 5 : 6;
+  static constexpr int kSlots = RES ? 2 : 1;           // 128 x 32 bf16 staging tiles a group
+  static constexpr int kOffY = kStages * kStageTiles;
+  static constexpr int kOffBar = kOffY + kPairGroups * kSlots * kYChunkBytes;
+  static constexpr int kNumBars = 2 * kStages + 2 * 2 + 1 + (RES ? kPairGroups * kSlots : 0);
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 64 + 1024;  // + alignment slack
   static constexpr int kTmemCols = 512;
@@ -94,19 +98,14 @@ __device__ __forceinline__ void store_chunk(const OutSlot &out, const CUtensorMa
   }
 }
 
-// The fp32 values alpha sa sw[n] sum of 32 columns n ... of one row (n % 8 == 0
-// keeps each read of four scales inside).
-__device__ __forceinline__ void scaled32(const uint32_t (&v)[32], float alpha, float sa,
-                                         const float *sw, int n, int N, float (&f)[32]) {
+// The values sa sw[j] v[j] of 32 columns of one row; lane j holds the scale of
+// column j (with so much shared memory in use there is no L1 to keep the scales
+// in: every lane reading all of them went to L2 each time).
+__device__ __forceinline__ void scaled32(const uint32_t (&v)[32], float sa, float sw,
+                                         float (&f)[32]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (n + 4 * j < N) s = __ldg(reinterpret_cast<const float4 *>(sw + n) + j);
-    const float s4[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f[4 * j + i] = __int2float_rn(static_cast<int>(v[4 * j + i])) * (sa * (alpha * s4[i]));
-  }
+  for (int j = 0; j < 32; ++j)
+    f[j] = __int2float_rn(static_cast<int>(v[j])) * (sa * __shfl_sync(0xFFFFFFFFu, sw, j));
 }
 
 // 32 gated outputs of one row (columns q0 ...), from g and u: the projections on
@@ -151,15 +150,16 @@ __device__ __forceinline__ void gated_chunk(const FfnArgs &a, const OutSlot &out
   gated_out(a, out, tm_y, tm_g, tm_u, g, up, q0, m0);
 }
 
-template <bool GATED>
+template <bool GATED, bool RES>
 __global__ void __launch_bounds__(kLinPairThreads, 1)
     lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                     const __grid_constant__ CUtensorMap tm_w0,
                     const __grid_constant__ CUtensorMap tm_w1,
                     const __grid_constant__ CUtensorMap tm_y,
-                    const __grid_constant__ CUtensorMap tm_g,
+                    const __grid_constant__ CUtensorMap tm_g,   // RES: the residual
                     const __grid_constant__ CUtensorMap tm_u, const FfnArgs a) {
-  using L = LinPairSmem;
+  static_assert(!(GATED && RES), "the gated block has no residual");
+  using L = LinPairSmem<RES>;
   constexpr int kStages = L::kStages, kAcc = 2;
   constexpr int kTileN = GATED ? 128 : 256;  // outputs of a tile
   extern __shared__ uint8_t smem_raw[];
@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
   uint64_t *tfull = empty + kStages;
   uint64_t *tempty = tfull + kAcc;
   uint64_t *drain = tempty + kAcc;
+  uint64_t *rbar = drain + 1;  // RES: a residual chunk has landed in its staging tile
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 4);
 
@@ -189,6 +190,8 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
       mbar_init(&tempty[i], 8 * kPairGroups);  // every epilogue warp of both CTAs
     }
     mbar_init(drain, 1);
+    if (RES)
+      for (int i = 0; i < kPairGroups * L::kSlots; ++i) mbar_init(&rbar[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_a);
@@ -281,20 +284,40 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
     const int quad = warp % 4;  // TMEM lane quadrant this warp may access
     const int row = quad * 32 + lane;
     const int group = (warp - 4) / 4;
-    const OutSlot out{smem + L::kOffY + group * kYChunkBytes, row, group,
+    const OutSlot out{smem + L::kOffY + group * L::kSlots * kYChunkBytes, row, group,
                       static_cast<int>(threadIdx.x % 128)};
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
+    uint32_t rphase = 0;  // residual barriers' parity: the same for all
     griddep_wait();  // scales, bias and residual may come from the kernel before
     for (int unit = pair; unit < total_units; unit += num_pairs) {
       const UnitPos u = unit_pos(a, unit);
       const int m0 = (2 * u.tp + static_cast<int>(rank)) * 128, m = m0 + row;
       const int n0 = u.tq * kTileN;
-      const bool mok = m < a.M;
-      const float sa = mok ? __ldg(a.sa + u.b * a.sa_bstride + m) : 0.0f;
+      // what the outputs need besides the sums, fetched while the sums are formed
+      const float sa = m < a.M ? __ldg(a.sa + u.b * a.sa_bstride + m) : 0.0f;
+      float sw[2], bias[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // gated: the group's one chunk of both weights; plain: its two chunks
+        const int n = n0 + (GATED ? group : group + kPairGroups * i) * 32 + lane;
+        sw[i] = n < a.N ? a.alpha * __ldg(a.sw[GATED ? i : 0] + u.b * a.sw_bstride + n) : 0.0f;
+        bias[i] = !GATED && a.bias && n < a.N ? __bfloat162float(a.bias[n]) : 0.0f;
+      }
+      if (RES && out.tid == 0) {
+        bulk_wait_group_read<0>();  // earlier stores have read the staging tiles
+#pragma unroll
+        for (int i = 0; i < L::kSlots; ++i) {
+          uint64_t *bar = &rbar[group * L::kSlots + i];
+          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(kYChunkBytes));
+          tma_load_3d(out.slot + i * kYChunkBytes, &tm_g, bar,
+                      n0 + (group + kPairGroups * i) * 32, m0, a.res_bstride ? u.b : 0);
+        }
+      }
       __syncwarp();
       if (!mbar_wait_cluster(&tfull[acc], acc_phase, a.err, abort_flag, kWaitEpiFull)) break;
+      __syncwarp();
       tc_fence_after();
       const uint32_t t_row = tmem_base + acc * 256 + (static_cast<uint32_t>(quad * 32) << 16);
       const int nch = min(kTileN / 32, (a.N - n0 + 31) / 32);
@@ -311,62 +334,65 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
         if (lane == 0) mbar_arrive_cluster(lead_tempty + acc * 8);
         if (group < nch) {  // uniform
           float g[32], up[32];
-          scaled32(vg, a.alpha, sa, a.sw[0], q0, a.N, g);
-          scaled32(vu, a.alpha, sa, a.sw[1], q0, a.N, up);
+          scaled32(vg, sa, sw[0], g);
+          scaled32(vu, sa, sw[1], up);
           gated_out(a, out, &tm_y, &tm_g, &tm_u, g, up, q0, m0);
         }
       } else {
-#pragma unroll 1
-        for (int c = group; c < nch; c += kPairGroups) {
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = group + kPairGroups * i;
+          if (RES && !mbar_wait(&rbar[group * L::kSlots + i * (L::kSlots - 1)], rphase, a.err,
+                                abort_flag, kWaitEpiFull)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          if (c >= nch) continue;  // uniform
           const int q0 = n0 + c * 32;
           uint32_t v[32];
-          __syncwarp();
           tmem_ld_32x32b_x32(t_row + c * 32, v);
-          uint4 rv[4];
-          if (a.res) {
-            const __nv_bfloat16 *r =
-                a.res + u.b * a.res_bstride + static_cast<int64_t>(m) * a.ldres + q0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              rv[j] = mok && q0 + 8 * j < a.N ? *reinterpret_cast<const uint4 *>(r + 8 * j)
-                                              : make_uint4(0u, 0u, 0u, 0u);
-          }
           tmem_ld_wait();
           float f[32];
-          scaled32(v, a.alpha, sa, a.sw[0] + u.b * a.sw_bstride, q0, a.N, f);
+          scaled32(v, sa, sw[i], f);
           if (a.bias) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (q0 + 8 * j >= a.N) break;
-              const uint4 bv = __ldg(reinterpret_cast<const uint4 *>(a.bias + q0 + 8 * j));
-              const uint32_t w[4] = {bv.x, bv.y, bv.z, bv.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                f[8 * j + 2 * i] += bf16_bits_to_f32(w[i] & 0xFFFFu);
-                f[8 * j + 2 * i + 1] += bf16_bits_to_f32(w[i] >> 16);
-              }
-            }
+            for (int j = 0; j < 32; ++j) f[j] += __shfl_sync(0xFFFFFFFFu, bias[i], j);
           }
           if (a.act == 1) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = gelu_erf(f[j]);
-          }
-          if (a.res) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t w[4] = {rv[j].x, rv[j].y, rv[j].z, rv[j].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                f[8 * j + 2 * i] += bf16_bits_to_f32(w[i] & 0xFFFFu);
-                f[8 * j + 2 * i + 1] += bf16_bits_to_f32(w[i] >> 16);
-              }
-            }
+            for (int j = 0; j < 32; ++j) f[j] = gelu_gate(f[j]);
           }
           uint32_t o[16];
+          if constexpr (RES) {
+            // the row's residual, and its outputs in the same place
+            uint8_t *slot = out.slot + i * kYChunkBytes;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
-          store_chunk(out, &tm_y, q0, m0, a.M, u.b, o);
+            for (int j = 0; j < 4; ++j) {
+              uint4 *at = reinterpret_cast<uint4 *>(slot + row * 64 + ((j ^ ((row >> 1) & 3)) << 4));
+              const uint4 rv = *at;
+              const uint32_t w[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                o[k] = pack_bf16(f[8 * j + 2 * k] + bf16_bits_to_f32(w[k] & 0xFFFFu),
+                                 f[8 * j + 2 * k + 1] + bf16_bits_to_f32(w[k] >> 16));
+              *at = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            fence_proxy_async_smem();
+            group_sync(group);
+            if (out.tid == 0 && m0 < a.M) {
+              tma_store_3d(&tm_y, slot, q0, m0, u.b);
+              bulk_commit_group();
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+            store_chunk(out, &tm_y, q0, m0, a.M, u.b, o);
+          }
         }
+        if (!ok) break;
+        rphase ^= 1;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(lead_tempty + acc * 8);
