@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       uint32_t phase = 0, acc_phase = 0, set_phase = 0;
       bool ok = true;
       for (int unit = pair; unit < total_units && ok; unit += num_pairs) {
-        if (!mbar_wait_cluster(tempty, acc_phase ^ 1, a.err, abort_flag, kWaitMmaTmemEmpty)) break;
+        if (!mbar_wait(tempty, acc_phase ^ 1, a.err, abort_flag, kWaitMmaTmemEmpty)) break;
         acc_phase ^= 1;
         tc_fence_after();
         for (int kt = 0; kt < a.kt_total; ++kt) {
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       const int m0 = (2 * u.tp + static_cast<int>(rank)) * 128;
       const int q0 = u.tq * kMxOut + group * 32;
       __syncwarp();
-      if (!mbar_wait_cluster(tfull, acc_phase, a.err, abort_flag, kWaitEpiFull)) break;
+      if (!mbar_wait(tfull, acc_phase, a.err, abort_flag, kWaitEpiFull)) break;
       acc_phase ^= 1;
       __syncwarp();
       tc_fence_after();
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(lead_tempty);
+      if (lane == 0) mbar_arrive_pair(lead_tempty);
       if (q0 < a.N)  // uniform
         gated_chunk(a, out, &tm_y, &tm_g, &tm_u, vg, vu, q0, m0);
     }

@@ -66,6 +66,13 @@ __device__ __forceinline__ void tc_commit2_both(uint64_t *bar) {
       : "memory");
 }
 
+// Arrive on an mbarrier given by its shared::cluster address, ordering nothing but
+// what tcgen05.fence::before_thread_sync has: no memory passes hands by it, and a
+// release at cluster scope would wait for the epilogue's stores.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Named barrier of one epilogue group's 128 threads.
 __device__ __forceinline__ void group_sync(int group) {
   __syncwarp();
@@ -248,7 +255,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int unit = pair; unit < total_units && ok; unit += num_pairs) {
-        if (!mbar_wait_cluster(&tempty[acc], acc_phase ^ 1, a.err, abort_flag, kWaitMmaTmemEmpty))
+        if (!mbar_wait(&tempty[acc], acc_phase ^ 1, a.err, abort_flag, kWaitMmaTmemEmpty))
           break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * 256;
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
         }
       }
       __syncwarp();
-      if (!mbar_wait_cluster(&tfull[acc], acc_phase, a.err, abort_flag, kWaitEpiFull)) break;
+      if (!mbar_wait(&tfull[acc], acc_phase, a.err, abort_flag, kWaitEpiFull)) break;
       __syncwarp();
       tc_fence_after();
       const uint32_t t_row = tmem_base + acc * 256 + (static_cast<uint32_t>(quad * 32) << 16);
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_tempty + acc * 8);
+        if (lane == 0) mbar_arrive_pair(lead_tempty + acc * 8);
         if (group < nch) {  // uniform
           float g[32], up[32];
           scaled32(vg, sa, sw[0], g);
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
         rphase ^= 1;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_tempty + acc * 8);
+        if (lane == 0) mbar_arrive_pair(lead_tempty + acc * 8);
       }
       if (++acc == kAcc) {
         acc = 0;
