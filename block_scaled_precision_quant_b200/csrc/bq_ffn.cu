@@ -277,12 +277,14 @@ struct Call {
 
 // Sums of int8 products stay below 2^31: K 128 128 < 2^31.
 constexpr int64_t kMaxInt8K = (int64_t{1} << 17) - 1;
+// Row numbers of the tile behind the last one still fit 32 bits.
+constexpr int64_t kMaxRows = 0x7FFFFE00;
 
 // Checks of the operands and of the sizes.
 int check_operands(const Call& c) {
   const bool i8 = c.kind == kInt8;
   if (c.M < 0 || c.N < 0 || c.K <= 0 || c.K % (i8 ? 16 : 32) != 0 || c.N % 8 != 0 ||
-      c.M > 0x7FFFFFFF || c.N > 0x7FFFFFFF || c.K > 0x7FFFFFFF || (i8 && c.K > kMaxInt8K) ||
+      c.M > kMaxRows || c.N > kMaxRows || c.K > 0x7FFFFFFF || (i8 && c.K > kMaxInt8K) ||
       (c.kind == kMxfp4 && c.K % 128 != 0) || c.batch.count < 0 || c.batch.count > 65535)
     return BQ_ERR_SHAPE;
   return BQ_OK;
@@ -422,7 +424,14 @@ int bq_act_quant_int8(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, voi
   Device dev;
   const int st = bqh::current_device(&dev);
   if (st != BQ_OK || M == 0) return st;
-  return launch(bq::i8_quant_kernel, dim3(static_cast<unsigned>(M)), 256, 0, 1, stream,
+  // Many short rows get a warp each (quant_i8.cuh; 600 x 2048: 2.5 us with blocks, 2.3
+  // with warps; of longer rows it takes more: 2048 x 4096: 6.0 and 7.1, 8192 x 4096: 24.2
+  // and 18.7).
+  const bool warps = K <= 2048 ? M >= 4 * dev.num_sms : K <= 4096 && M >= 32 * dev.num_sms;
+  return launch(!warps      ? bq::i8_quant_kernel
+                : K <= 2048 ? bq::i8_quant_warp_kernel<8>
+                            : bq::i8_quant_warp_kernel<16>,
+                dim3(static_cast<unsigned>(warps ? ceil_div(M, 8) : M)), 256, 0, 1, stream,
                 static_cast<const __nv_bfloat16*>(x_bf16), M, K, ldx,
                 static_cast<uint8_t*>(q_s8), scale, d_status);
 }

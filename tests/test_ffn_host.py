@@ -37,7 +37,8 @@ def test_product_refusals(L):
         assert product(L, **{k: None}) == bq.BQ_ERR_NULL
         assert product(L, **{k: P + 2}) == bq.BQ_ERR_ALIGN
     assert product(L, sb=P + 4) == bq.BQ_ERR_ALIGN
-    for kw in (dict(K=24), dict(K=0), dict(N=12), dict(M=-1), dict(K=131072), dict(N=1 << 32)):
+    for kw in (dict(K=24), dict(K=0), dict(N=12), dict(M=-1), dict(K=131072), dict(N=1 << 32),
+               dict(M=0x7FFFFF00)):
         assert product(L, **kw) == bq.BQ_ERR_SHAPE
     E = bq.Epilogue
     assert product(L, epi=E(None, None, 0, 1.0, 2, None, None)) == bq.BQ_ERR_INVALID

@@ -313,6 +313,39 @@ def test_training_step_captured_and_replayed():
     assert eager[0].shape == (M, 2 * N)
 
 
+@pytest.mark.parametrize("kind", ["mxfp8", "int8"])
+@pytest.mark.parametrize("M", [40, 600])
+def test_two_streams_at_once(kind, M):
+    N, K = 512, 1024
+    a = Operand("int8" if kind == "int8" else "mxfp8", M, K, 1)
+    w, v = Operand(kind, N, K, 2), Operand(kind, N, K, 3)
+
+    def call():
+        return bq.gemm_gated(KIND[kind], a.q, a.sf, w.q, w.sf, v.q, v.sf, M, N, K, alpha=0.01)
+
+    one = call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(20):
+        for st in streams:
+            with torch.cuda.stream(st):
+                outs.append(call())
+    torch.cuda.synchronize()
+    bq.device_status()
+    assert all(torch.equal(one, y) for y in outs)
+
+
+def test_one_weight_as_both():
+    """The same operand as gate and up projection."""
+    M, N, K = 300, 200, 256
+    a, w = Operand("mxfp8", M, K, 1), Operand("mxfp8", N, K, 2)
+    b = bq.gemm_gated(bq.W_MXFP8, a.q, a.sf, w.q, w.sf, w.q, w.sf, M, N, K, alpha=0.01,
+                      keep_projections=True)
+    bq.device_status()
+    assert torch.equal(b[1][:, :N], b[1][:, N:])
+
+
 def test_empty_calls():
     a, w = Operand("mxfp8", 4, 32, 1), Operand("mxfp8", 8, 32, 2)
     y = bq.gemm_gated(bq.W_MXFP8, a.q[:0], a.sf, w.q, w.sf, w.q, w.sf, 0, 8, 32)

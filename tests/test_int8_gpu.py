@@ -26,7 +26,10 @@ def check_quant(x, q, s):
 # one row, rows shorter and longer than a block's registers, odd tails of every kind
 @pytest.mark.parametrize("M,K", [(1, 16), (1, 4096), (3, 48), (7, 240), (41, 1536), (130, 2064),
                                  (33, 8192), (5, 8208), (2, 16400), (3, 65552), (1, 131056),
-                                 (2500, 272)])
+                                 (2500, 272),
+                                 # a warp to a row: short rows and longer ones
+                                 (595, 16), (1201, 2048), (700, 992), (4740, 2064),
+                                 (4737, 4096)])
 def test_quant_rows(M, K):
     x = rows(M, K, M + K)
     q, s = bq.act_quant_int8(x)
@@ -63,22 +66,23 @@ def test_quant_small_zero_and_large_rows():
     assert int(q[0].abs().max()) == 0 and int(q[1].min()) == 127
 
 
-def test_quant_row_stride_outputs_and_status():
-    wide = rows(45, 200, 3)
+@pytest.mark.parametrize("M", [45, 605])
+def test_quant_row_stride_outputs_and_status(M):
+    wide = rows(M, 200, 3)
     x = wide[:, :160]
-    q = torch.full((46, 160), 77, dtype=torch.int8, device="cuda")
-    s = torch.full((46,), 5.0, device="cuda")
+    q = torch.full((M + 1, 160), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((M + 1,), 5.0, device="cuda")
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    bq.act_quant_int8(x, q=q[:45], scale=s[:45], status=st)
-    check_quant(x, q[:45], s[:45])
-    assert bool((q[45] == 77).all()) and float(s[45]) == 5.0 and int(st) == 0
+    bq.act_quant_int8(x, q=q[:M], scale=s[:M], status=st)
+    check_quant(x, q[:M], s[:M])
+    assert bool((q[M] == 77).all()) and float(s[M]) == 5.0 and int(st) == 0
     for bad in (float("inf"), float("-inf"), float("nan")):
         y = x.clone()
-        y[44, 159] = bad
+        y[M - 1, 159] = bad
         st.zero_()
         q2, s2 = bq.act_quant_int8(y, status=st)
         assert int(st) == 1
-        check_quant(y[:44], q2[:44], s2[:44])  # the other rows stand
+        check_quant(y[:M - 1], q2[:M - 1], s2[:M - 1])  # the other rows stand
 
 
 def product(M, N, K, seed, bias=False, res=False, act=0, alpha=1.0, config=None, ldres=None):
@@ -227,20 +231,33 @@ def test_linear_layer_chain_captured_and_replayed():
     bq.device_status()
 
 
-def test_two_streams_at_once():
-    ops = [(Operand("int8", 64, 2048, s), Operand("int8", 1024, 2048, s + 50)) for s in range(2)]
-    one = [bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, 64, 1024, 2048) for a, b in ops]
+@pytest.mark.parametrize("M", [64, 700])
+def test_two_streams_at_once(M):
+    ops = [(Operand("int8", M, 2048, s), Operand("int8", 1024, 2048, s + 50)) for s in range(2)]
+    one = [bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, M, 1024, 2048) for a, b in ops]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in ops]
     outs = [[], []]
     for _ in range(20):
         for i, (st, (a, b)) in enumerate(zip(streams, ops)):
             with torch.cuda.stream(st):
-                outs[i].append(bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, 64, 1024, 2048))
+                outs[i].append(bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, M, 1024, 2048))
     torch.cuda.synchronize()
     bq.device_status()
     for i in range(2):
         assert all(torch.equal(one[i], y) for y in outs[i])
+
+
+def test_residual_in_place():
+    """y may be the residual itself: a chunk's residual is read before it is written."""
+    for M in (41, 300):
+        a, b = Operand("int8", M, 528, 1), Operand("int8", 648, 528, 2)
+        r = (torch.randn((M, 648), device="cuda") * 3).to(torch.bfloat16)
+        ref = bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, M, 648, 528, residual=r)
+        got = r.clone()
+        bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, M, 648, 528, residual=got, y=got)
+        bq.device_status()
+        assert torch.equal(got, ref)
 
 
 def test_empty_calls():
