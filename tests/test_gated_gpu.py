@@ -80,6 +80,21 @@ def test_forward_pair_tiles(kind, M, N, K):
     forward(kind, M, N, K, ACTS[(M + 1) % 2], M + N, keep=M != 128, config=bq.config(swap_ab=0))
 
 
+# more tiles than pairs of SMs, K blocks that end anywhere in the rings of operands
+# (5 or 6) and scales (4 to a stage)
+@pytest.mark.parametrize("kind", list(KIND))
+@pytest.mark.parametrize("K", [128, 640, 1408])
+def test_forward_pair_tiles_in_several_waves(kind, K):
+    forward(kind, 2900, 1672, K, ACTS[K % 3 == 2], K, keep=K == 640, config=bq.config(swap_ab=0))
+
+
+@pytest.mark.parametrize("kind", ["mxfp4", "int8"])
+def test_quantized_hidden_in_several_waves(kind):
+    outs, _, _ = forward(kind, 2900, 1696, 384, bq.BQ_GATE_GELU, 3, quant=True)
+    q, sf = bq.act_quant(outs[0])
+    assert torch.equal(outs[1], q) and torch.equal(outs[2], sf)
+
+
 @pytest.mark.parametrize("kind", list(KIND))
 @pytest.mark.parametrize("M,N,K", [(1, 32, 128), (41, 1536, 512), (70, 160, 384), (130, 96, 256),
                                    (300, 416, 640)])

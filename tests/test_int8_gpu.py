@@ -136,6 +136,14 @@ def test_pair_tiles(M, N, K, bias, res, act):
     product(M, N, K, M + K, bias, res, act, 0.5, bq.config(swap_ab=0), ldres=N + 8)
 
 
+# more tiles than pairs of SMs: every pair works on several, with K blocks that end
+# anywhere in the operand ring
+@pytest.mark.parametrize("K", [64, 640, 1424])
+@pytest.mark.parametrize("bias,res,act", [(False, False, 0), (True, True, 1)])
+def test_pair_tiles_in_several_waves(K, bias, res, act):
+    product(2900, 3336, K, K, bias, res, act, 0.5, bq.config(swap_ab=0))
+
+
 def test_pair_tiles_equal_swap_tiles():
     a, b = Operand("int8", 300, 1552, 5), Operand("int8", 776, 1552, 6)
     ys = [bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, 300, 776, 1552, config=c)
