@@ -373,9 +373,10 @@ def quant_transposed(x, fmt=BQ_FMT_E4M3, stochastic=False, seed=0, q=None, sf_mm
         raise ValueError("x must be a bf16 [R, C] tensor with unit column stride")
     R, C = x.shape
     if q is None:
-        q = torch.empty((C, R), dtype=torch.uint8, device=x.device)
+        q = torch.empty_strided((C, R), (R, 1), dtype=torch.uint8, device=x.device)
     if sf_mma is None:
-        sf_mma = torch.empty((max(sf_bytes(C, R), 1),), dtype=torch.uint8, device=x.device)
+        sf_mma = torch.empty_strided((max(sf_bytes(C, R), 1),), (1,), dtype=torch.uint8,
+                                     device=x.device)
     _check(lib().bq_quant_transposed(_ptr(x), R, C, x.stride(0), int(fmt),
                                      BQ_ROUND_STOCHASTIC if stochastic else BQ_ROUND_NEAREST,
                                      int(seed) & (2 ** 64 - 1), _ptr(q), _ptr(sf_mma),
@@ -475,7 +476,8 @@ def gemm(weight_kind, a_q, a_sf, b, b_sf, M, N, K, y=None, bias=None, residual=N
     if not write_y and not quantize_out:
         raise ValueError("write_y=False needs quantize_out=True")
     if y is None and write_y:
-        y = torch.empty(shape, dtype=torch.bfloat16, device=a_q.device)
+        y = (torch.empty_strided((M, N), (N, 1), dtype=torch.bfloat16, device=a_q.device)
+             if batch is None else torch.empty(shape, dtype=torch.bfloat16, device=a_q.device))
     if quantize_out:
         if q_out is None:
             q_out = torch.empty(shape, dtype=torch.uint8, device=a_q.device)

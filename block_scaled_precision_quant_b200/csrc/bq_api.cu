@@ -841,7 +841,7 @@ const char* bq_status_string(int status) {
   }
 }
 
-int bq_version(void) { return 100; }
+int bq_version(void) { return 200; }
 
 size_t bq_sf_bytes(int64_t rows, int64_t K) {
   if (rows < 0 || K <= 0 || K % 32 != 0) return 0;

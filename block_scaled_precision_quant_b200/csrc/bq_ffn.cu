@@ -112,6 +112,21 @@ int output_map(CUtensorMap* m, const void* y, int64_t M, int64_t N, int64_t ld, 
   return r == CUDA_SUCCESS ? BQ_OK : BQ_ERR_ALIGN;
 }
 
+// A bf16 matrix [rows][ld] of `cols` columns: boxes of 128 x 128, no swizzle.
+int matrix_map(CUtensorMap* m, const void* x, int64_t rows, int64_t cols, int64_t ld) {
+  auto encode = bqh::tensor_map_encoder();
+  if (!encode) return BQ_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * ld)};
+  const cuuint32_t box[2] = {128u, 128u};
+  const cuuint32_t step[2] = {1u, 1u};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims,
+                            strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? BQ_OK : BQ_ERR_ALIGN;
+}
+
 // ---------------------------------------------------------------- schedule --
 
 struct Plan {
@@ -527,7 +542,8 @@ int bq_gated_grad_quant(const void* dh_bf16, int64_t ld_dh, const void* gu_bf16,
                         bq_stream_t stream) {
   if (act != BQ_GATE_SILU && act != BQ_GATE_GELU) return BQ_ERR_INVALID;
   if (rounding != BQ_ROUND_NEAREST && rounding != BQ_ROUND_STOCHASTIC) return BQ_ERR_INVALID;
-  if (M < 0 || M % 32 != 0 || N <= 0 || N % 32 != 0 || ld_dh < N || ld_gu < 2 * N)
+  if (M < 0 || M > kMaxRows || M % 32 != 0 || N <= 0 || N % 32 != 0 || ld_dh < N ||
+      ld_gu < 2 * N)
     return BQ_ERR_SHAPE;
   const int64_t groups = ceil_div(M, 128) * 4, tiles = ceil_div(N, 64);
   if (groups > 0x7FFFFFFF || ceil_div(tiles, 2) > 65535) return BQ_ERR_SHAPE;
@@ -555,11 +571,16 @@ int bq_gated_grad_quant(const void* dh_bf16, int64_t ld_dh, const void* gu_bf16,
         return BQ_ERR_CUDA;
       ready[dev.index][act] = true;
     }
+    CUtensorMap th, tg, tu;
+    int mst = matrix_map(&th, dh, M, N, ld_dh);
+    if (mst == BQ_OK) mst = matrix_map(&tg, gu, M, N, ld_gu);
+    if (mst == BQ_OK) mst = matrix_map(&tu, gu + N, M, N, ld_gu);
+    if (mst != BQ_OK) return mst;
     return launch(kern,
                   dim3(static_cast<unsigned>(ceil_div(M, 128)),
                        static_cast<unsigned>(ceil_div(N, 128))),
-                  256, bq::GradSmem::kBytes, 1, stream, dh, ld_dh, gu, ld_gu, M, N, qr, sr, qt, st8, d,
-                  d_status);
+                  bq::kGradThreads, bq::GradSmem::kBytes, 1, stream, th, tg, tu, M, N, qr, sr, qt, st8, d,
+                  d_status, dev.err);
   }
   auto kern = act == BQ_GATE_SILU ? bq::gated_grad_sr_kernel<bq::kGateSilu>
                                   : bq::gated_grad_sr_kernel<bq::kGateGelu>;

@@ -193,23 +193,44 @@ __global__ void __launch_bounds__(256, 2) gated_grad_sr_kernel(
 
 // ---- round to nearest ------------------------------------------------------
 //
-// A block owns 128 rows x 128 columns of F and works on them three times, each
-// time with the ownership that needs no exchange between threads:
-//   1. eight columns of a row a thread (three 16-byte loads): dG and dU as bf16
-//      into two tiles in shared memory;
+// A block owns 128 rows x 128 columns of F: three TMA loads bring dH, g and u into
+// shared memory (zeros outside), and it works on them three times, each time with
+// the ownership that needs no exchange between threads:
+//   1. eight columns of a row a thread: dG and dU as bf16 in the places of g and u;
 //   2. 16 columns of a row a thread, two threads a group (one shuffle for its
 //      maximum): the row-wise codes, a row's 128 bytes by eight threads;
 //   3. two columns x 32 rows a thread, whole groups: the transposed codes, which
 //      turn around through the tiles' memory and leave as 128-byte lines.
-// 35 instructions an element instead of the 63 of a version that kept one
-// ownership and met by shuffles.  Floor: 6 bytes read and 4.1 written for each
-// element of F.
+// Floor: 6 bytes read and 4.1 written for each element of F.  Bound by the
+// instructions it issues, some 45 an element (63 in a version that kept one
+// ownership and met by shuffles).
 struct GradSmem {
-  static constexpr int kTile = 128 * 256;      // [128 rows][128 bf16]
-  static constexpr int kOffSfr = 2 * kTile;    // [2][128 rows][4 groups]
+  static constexpr int kTile = 128 * 256;         // [128 rows][128 bf16]: g, u, dH
+  static constexpr int kOffSfr = 3 * kTile;       // [2][128 rows][4 groups]
   static constexpr int kOffSft = kOffSfr + 1024;  // [2][128 columns][4 groups]
-  static constexpr int kBytes = kOffSft + 1024;
+  static constexpr int kOffBar = kOffSft + 1024;
+  static constexpr int kBytes = kOffBar + 16;
 };
+
+// Four E5M2 codes (round to nearest even, saturating) in one word, a in the low byte:
+// packed by the conversions themselves.
+__device__ __forceinline__ uint32_t e5m2x4(float a, float b, float c, float d) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(w)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return w;
+}
+
+// The larger magnitudes of two bf16 pairs (their signs are of no use; NaN wins).
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 // Byte offset of 16-byte piece q (8 columns) of row r of a tile: the pieces of a
 // row's second half are swapped in pairs, so eight threads that read every second
@@ -224,95 +245,100 @@ __device__ __forceinline__ uint32_t code_at(int r, int q) {
   return static_cast<uint32_t>(r * 128 + ((q ^ ((r >> 1) & 7)) << 4));
 }
 
+constexpr int kGradThreads = 512;
+
 template <int ACT>
-__global__ void __launch_bounds__(256, 3) gated_grad_rne_kernel(
-    const __nv_bfloat16 *__restrict__ dh, int64_t ld_dh, const __nv_bfloat16 *__restrict__ gu,
-    int64_t ld_gu, int64_t R, int64_t F, uint8_t *__restrict__ q_row, uint8_t *__restrict__ sf_row,
-    uint8_t *__restrict__ q_t, uint8_t *__restrict__ sf_t, __nv_bfloat16 *__restrict__ d_out,
-    int *__restrict__ status) {
+__global__ void __launch_bounds__(kGradThreads, 2) gated_grad_rne_kernel(
+    const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ CUtensorMap tm_g,
+    const __grid_constant__ CUtensorMap tm_u, int64_t R, int64_t F, uint8_t *__restrict__ q_row,
+    uint8_t *__restrict__ sf_row, uint8_t *__restrict__ q_t, uint8_t *__restrict__ sf_t,
+    __nv_bfloat16 *__restrict__ d_out, int *__restrict__ status, int *__restrict__ err) {
   extern __shared__ __align__(128) uint8_t grad_smem[];
+  __shared__ int abort_flag;
   uint8_t *sm = grad_smem;
+  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + GradSmem::kOffBar);
   const int tid = threadIdx.x;
   const int64_t C = 2 * F, b0 = static_cast<int64_t>(blockIdx.x) * 128;  // rows
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * 128;             // columns of F
   const int ncols = static_cast<int>(F - c0 < 128 ? F - c0 : 128);       // multiples of 32
   const int nrows = static_cast<int>(R - b0 < 128 ? R - b0 : 128);
-  griddep_wait();
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    griddep_wait();
+    mbar_arrive_expect_tx(bar, 3 * GradSmem::kTile);
+    const int x = static_cast<int>(c0), y = static_cast<int>(b0);
+    tma_load_2d(sm, &tm_g, bar, x, y);
+    tma_load_2d(sm + GradSmem::kTile, &tm_u, bar, x, y);
+    tma_load_2d(sm + 2 * GradSmem::kTile, &tm_dh, bar, x, y);
+  }
+  __syncthreads();
+  griddep_wait();  // the kernel before may still read what this one writes
   griddep_launch_dependents();
+  if (!mbar_wait(bar, 0, err, &abort_flag, kWaitLanding)) return;
 
   {
-    const int q = tid & 15, r1 = tid >> 4;  // rows r1, r1 + 16, ...
-    const bool col_ok = 8 * q < ncols;
-    const __nv_bfloat16 *ph = dh + (b0 + r1) * ld_dh + c0 + 8 * q;
-    const __nv_bfloat16 *pg = gu + (b0 + r1) * ld_gu + c0 + 8 * q;
+    const int q = tid & 15, r1 = tid >> 4;  // rows r1, r1 + 32, ...: a warp holds whole rows
+    const uint8_t *src = sm + r1 * 256 + q * 16;
 #pragma unroll 1
     for (int k = 0; k < 4; ++k) {
-      uint4 th[2], tg[2], tu[2];
+      const uint4 tg = *reinterpret_cast<const uint4 *>(src + k * 32 * 256);
+      const uint4 tu = *reinterpret_cast<const uint4 *>(src + GradSmem::kTile + k * 32 * 256);
+      const uint4 th = *reinterpret_cast<const uint4 *>(src + 2 * GradSmem::kTile + k * 32 * 256);
+      const uint32_t h4[4] = {th.x, th.y, th.z, th.w}, g4[4] = {tg.x, tg.y, tg.z, tg.w},
+                     u4[4] = {tu.x, tu.y, tu.z, tu.w};
+      uint32_t og[4], ou[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        th[i] = tg[i] = tu[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (col_ok && r1 + 32 * k + 16 * i < nrows) {
-          th[i] = __ldg(reinterpret_cast<const uint4 *>(ph + i * 16 * ld_dh));
-          tg[i] = __ldg(reinterpret_cast<const uint4 *>(pg + i * 16 * ld_gu));
-          tu[i] = __ldg(reinterpret_cast<const uint4 *>(pg + i * 16 * ld_gu + F));
-        }
+      for (int j = 0; j < 4; ++j) {
+        float dg[2], du[2];
+        gate_grad<ACT>(__uint_as_float(h4[j] << 16), __uint_as_float(g4[j] << 16),
+                       __uint_as_float(u4[j] << 16), dg[0], du[0]);
+        gate_grad<ACT>(__uint_as_float(h4[j] & 0xFFFF0000u), __uint_as_float(g4[j] & 0xFFFF0000u),
+                       __uint_as_float(u4[j] & 0xFFFF0000u), dg[1], du[1]);
+        og[j] = pack_bf16(dg[0], dg[1]);
+        ou[j] = pack_bf16(du[0], du[1]);
       }
-      ph += 32 * ld_dh;
-      pg += 32 * ld_gu;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t h4[4] = {th[i].x, th[i].y, th[i].z, th[i].w};
-        const uint32_t g4[4] = {tg[i].x, tg[i].y, tg[i].z, tg[i].w};
-        const uint32_t u4[4] = {tu[i].x, tu[i].y, tu[i].z, tu[i].w};
-        uint32_t og[4], ou[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float dg[2], du[2];
-          gate_grad<ACT>(__uint_as_float(h4[j] << 16), __uint_as_float(g4[j] << 16),
-                         __uint_as_float(u4[j] << 16), dg[0], du[0]);
-          gate_grad<ACT>(__uint_as_float(h4[j] & 0xFFFF0000u),
-                         __uint_as_float(g4[j] & 0xFFFF0000u),
-                         __uint_as_float(u4[j] & 0xFFFF0000u), dg[1], du[1]);
-          og[j] = pack_bf16(dg[0], dg[1]);
-          ou[j] = pack_bf16(du[0], du[1]);
-        }
-        const int r = r1 + 32 * k + 16 * i;
-        *reinterpret_cast<uint4 *>(sm + grad_at(r, q)) = make_uint4(og[0], og[1], og[2], og[3]);
-        *reinterpret_cast<uint4 *>(sm + GradSmem::kTile + grad_at(r, q)) =
-            make_uint4(ou[0], ou[1], ou[2], ou[3]);
-        if (d_out && col_ok && r < nrows) {
-          __nv_bfloat16 *d = d_out + (b0 + r) * C + c0 + 8 * q;
-          *reinterpret_cast<uint4 *>(d) = make_uint4(og[0], og[1], og[2], og[3]);
-          *reinterpret_cast<uint4 *>(d + F) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-        }
+      const int r = r1 + 32 * k;
+      __syncwarp();  // the row has been read
+      *reinterpret_cast<uint4 *>(sm + grad_at(r, q)) = make_uint4(og[0], og[1], og[2], og[3]);
+      *reinterpret_cast<uint4 *>(sm + GradSmem::kTile + grad_at(r, q)) =
+          make_uint4(ou[0], ou[1], ou[2], ou[3]);
+      if (d_out && 8 * q < ncols && r < nrows) {
+        __nv_bfloat16 *d = d_out + (b0 + r) * C + c0 + 8 * q;
+        *reinterpret_cast<uint4 *>(d) = make_uint4(og[0], og[1], og[2], og[3]);
+        *reinterpret_cast<uint4 *>(d + F) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
       }
     }
   }
   __syncthreads();
 
-  {  // along the columns of d: 16 columns of rows r1, r1 + 32, ... of both halves
+  {  // along the columns of d: 16 columns of rows r1, r1 + 64 of both halves
     const int j = tid & 7, r1 = tid >> 3;
     uint32_t bad = 0;
 #pragma unroll 1
-    for (int k = 0; k < 8; ++k) {
-      const int half = k >> 2, r = r1 + 32 * (k & 3);
+    for (int k = 0; k < 4; ++k) {
+      const int half = k >> 1, r = r1 + 64 * (k & 1);
       const uint8_t *tile = sm + half * GradSmem::kTile;
       const uint4 a = *reinterpret_cast<const uint4 *>(tile + grad_at(r, 2 * j));
       const uint4 b = *reinterpret_cast<const uint4 *>(tile + grad_at(r, 2 * j + 1));
       const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint32_t mx = bf16_amax_bits(w, bad);
+      const uint32_t m2 =
+          absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(w[0], w[1]), absmax_bf16x2(w[2], w[3])),
+                        absmax_bf16x2(absmax_bf16x2(w[4], w[5]), absmax_bf16x2(w[6], w[7]))) &
+          0x7FFF7FFFu;
+      uint32_t mx = max(m2 & 0xFFFFu, m2 >> 16);
+      bad |= mx >= 0x7F80u ? 1u : 0u;
       mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
       const int e = mx_exponent_e5m2(mx);
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       uint32_t codes[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = e5m2x2(__fmul_rn(__uint_as_float(w[2 * i] << 16), inv),
-                                   __fmul_rn(__uint_as_float(w[2 * i] & 0xFFFF0000u), inv));
-        const uint32_t hi = e5m2x2(__fmul_rn(__uint_as_float(w[2 * i + 1] << 16), inv),
-                                   __fmul_rn(__uint_as_float(w[2 * i + 1] & 0xFFFF0000u), inv));
-        codes[i] = __byte_perm(lo, hi, 0x5410);
-      }
+      for (int i = 0; i < 4; ++i)
+        codes[i] = e5m2x4(__fmul_rn(__uint_as_float(w[2 * i] << 16), inv),
+                          __fmul_rn(__uint_as_float(w[2 * i] & 0xFFFF0000u), inv),
+                          __fmul_rn(__uint_as_float(w[2 * i + 1] << 16), inv),
+                          __fmul_rn(__uint_as_float(w[2 * i + 1] & 0xFFFF0000u), inv));
       if (r < nrows && 16 * j < ncols)
         *reinterpret_cast<uint4 *>(q_row + (b0 + r) * C + half * F + c0 + 16 * j) =
             make_uint4(codes[0], codes[1], codes[2], codes[3]);
@@ -322,19 +348,19 @@ __global__ void __launch_bounds__(256, 3) gated_grad_rne_kernel(
     }
     if (bad && status) atomicOr(status, 1);
   }
-  // along the rows: columns 2 p, 2 p + 1 of the 32-row group rg of both halves
-  const int p = tid & 63, rg = tid >> 6;
-  uint32_t out[2][2][8];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  // along the rows: columns 2 p, 2 p + 1 of the 32-row group rg of one half
+  const int p = tid & 63, rg = (tid >> 6) & 3, half = tid >> 8;
+  uint32_t out[2][8];
+  {
     const uint8_t *tile = sm + half * GradSmem::kTile + 4 * (p & 3);
     uint32_t w[32];
 #pragma unroll
     for (int r = 0; r < 32; ++r)
       w[r] = *reinterpret_cast<const uint32_t *>(tile + grad_at(rg * 32 + r, p >> 2));
-    uint32_t m = 0;
+    uint32_t m = w[0];
 #pragma unroll
-    for (int r = 0; r < 32; ++r) m = max_u16x2(m, w[r] & 0x7FFF7FFFu);
+    for (int r = 1; r < 32; ++r) m = absmax_bf16x2(m, w[r]);
+    m &= 0x7FFF7FFFu;
     const int e0 = mx_exponent_e5m2(m & 0xFFFFu), e1 = mx_exponent_e5m2(m >> 16);
     const bool ok = rg * 32 < nrows;
     uint8_t *sft = sm + GradSmem::kOffSft + (half * 128 + 2 * p) * 4 + rg;
@@ -343,39 +369,36 @@ __global__ void __launch_bounds__(256, 3) gated_grad_rne_kernel(
     const float inv0 = __uint_as_float(static_cast<uint32_t>(127 - e0) << 23);
     const float inv1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t c[4];  // rows 4 j .. 4 j + 3: column 2 p in the low byte
+    for (int j = 0; j < 8; ++j) {  // rows 4 j .. 4 j + 3
+      float lo[4], hi[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        c[t] = e5m2x2(__fmul_rn(__uint_as_float(w[4 * j + t] << 16), inv0),
-                      __fmul_rn(__uint_as_float(w[4 * j + t] & 0xFFFF0000u), inv1));
-      const uint32_t lo = __byte_perm(c[0], c[1], 0x5140), hi = __byte_perm(c[2], c[3], 0x5140);
-      out[half][0][j] = __byte_perm(lo, hi, 0x5410);
-      out[half][1][j] = __byte_perm(lo, hi, 0x7632);
+      for (int t = 0; t < 4; ++t) {
+        lo[t] = __fmul_rn(__uint_as_float(w[4 * j + t] << 16), inv0);
+        hi[t] = __fmul_rn(__uint_as_float(w[4 * j + t] & 0xFFFF0000u), inv1);
+      }
+      out[0][j] = e5m2x4(lo[0], lo[1], lo[2], lo[3]);
+      out[1][j] = e5m2x4(hi[0], hi[1], hi[2], hi[3]);
     }
   }
   __syncthreads();  // the tiles have been read
 #pragma unroll
-  for (int half = 0; half < 2; ++half)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        *reinterpret_cast<uint4 *>(sm + half * 16384 + code_at(2 * p + h, 2 * rg + q)) =
-            make_uint4(out[half][h][4 * q], out[half][h][4 * q + 1], out[half][h][4 * q + 2],
-                       out[half][h][4 * q + 3]);
+    for (int q = 0; q < 2; ++q)
+      *reinterpret_cast<uint4 *>(sm + half * 16384 + code_at(2 * p + h, 2 * rg + q)) = make_uint4(
+          out[h][4 * q], out[h][4 * q + 1], out[h][4 * q + 2], out[h][4 * q + 3]);
   __syncthreads();
 #pragma unroll
-  for (int i = tid; i < 2048; i += 256) {
-    const int half = i >> 10, c = (i >> 3) & 127, q = i & 7;
+  for (int i = tid; i < 2048; i += kGradThreads) {
+    const int hf = i >> 10, c = (i >> 3) & 127, q = i & 7;
     if (c < ncols && 16 * q < nrows)
-      *reinterpret_cast<uint4 *>(q_t + (half * F + c0 + c) * R + b0 + 16 * q) =
-          *reinterpret_cast<const uint4 *>(sm + half * 16384 + code_at(c, q));
+      *reinterpret_cast<uint4 *>(q_t + (hf * F + c0 + c) * R + b0 + 16 * q) =
+          *reinterpret_cast<const uint4 *>(sm + hf * 16384 + code_at(c, q));
   }
   const int64_t katoms_t = ((R >> 5) + 3) >> 2, katoms_r = ((C >> 5) + 3) >> 2;
-  {
-    const int half = tid >> 7, t = tid & 127;
-    const int64_t cd = half * F + c0, g = cd >> 5;  // first column and group in d
+  if (tid < 256) {
+    const int t = tid & 127;
+    const int64_t cd = (tid >> 7) * F + c0, g = cd >> 5;  // first column and group in d
     const uint8_t *sfr = sm + GradSmem::kOffSfr + tid * 4;
     const int ng = ncols >> 5;
     if (ng == 4 && (g & 3) == 0) {  // a word of a scale atom

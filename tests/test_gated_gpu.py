@@ -209,10 +209,27 @@ def test_grad_quant_strides_and_status():
     for x, y in zip(got, ref):
         assert torch.equal(x, y)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    bad = a.contiguous()
-    bad[M - 1, N - 1] = float("inf")
-    bq.gated_grad_quant(bad, b, status=st)
-    assert int(st) == 1
+    bq.gated_grad_quant(a, b, status=st)
+    assert int(st) == 0
+    for value in (float("inf"), float("-inf"), float("nan")):
+        for r, c in ((M - 1, N - 1), (0, 0), (33, 17)):
+            bad = a.contiguous()
+            bad[r, c] = value
+            st.zero_()
+            bq.gated_grad_quant(bad, b, status=st)
+            assert int(st) == 1, (value, r, c)
+
+
+def test_grad_quant_zero_and_signed_zero_groups():
+    """Groups of zeros keep the floor scale and the zeros' signs, as grad_quant_dual does."""
+    M, N = 64, 96
+    dh, gu = grads(M, N, 3)
+    dh[:32, :32] = 0.0
+    dh[32:, 32:64] = -0.0
+    d = torch.empty((M, 2 * N), dtype=torch.bfloat16, device="cuda")
+    got = bq.gated_grad_quant(dh, gu, d=d)
+    for x, y in zip(got, bq.grad_quant_dual(d)):
+        assert torch.equal(x, y)
 
 
 def test_grad_far_gates():
