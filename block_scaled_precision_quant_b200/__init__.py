@@ -457,9 +457,10 @@ def gemm(weight_kind, a_q, a_sf, b, b_sf, M, N, K, y=None, bias=None, residual=N
     E2M1 activations a_q [.., M, K/2] from act_quant_mxfp4), W_NVFP4 (packed
     E2M1 activations and weights with E4M3 scales per 16, from act_quant_nvfp4;
     alpha = 1 / (g_a g_b) undoes the per-tensor scales), W_GRAD (E5M2
-    gradient codes a_q [.., M, K], MXFP8 b) or W_INT8 (gemm_int8_int8).  batch: None or a dict with 'count' and byte
-    strides ('stride_a', 'stride_a_sf', 'stride_b', 'stride_b_sf', 'stride_y',
-    'stride_res'; 0 broadcasts).  config: GemmConfig or None (auto).
+    gradient codes a_q [.., M, K], MXFP8 b) or W_INT8 (gemm_int8_int8).
+    batch: None or a dict with 'count' and byte strides ('stride_a',
+    'stride_a_sf', 'stride_b', 'stride_b_sf', 'stride_y', 'stride_res'; 0
+    broadcasts).  config: GemmConfig or None (auto).
     quantize_out: also return y quantized for the next GEMM (E4M3 codes
     [.., M, N] u8 and MMA-layout scales, exactly act_quant of y, written to
     q_out / sf_out when given); then returns (y or None, q, sf), with no bf16

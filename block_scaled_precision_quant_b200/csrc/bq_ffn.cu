@@ -406,8 +406,8 @@ int run(const Call& c, bool gated, bool empty, const bq_gemm_config* cfg, bq::Ff
                     c.batch.stride_res);
     if (st != BQ_OK) return st;
     return launch_pairs(bq::lin_pair_kernel<false, true>, ready[3], kT,
-                        bq::LinPairSmem<true>::kBytes, pl, dev, stream, ta, tw[0], tw[0], ty, tr, tu,
-                        *g);
+                        bq::LinPairSmem<true>::kBytes, pl, dev, stream, ta, tw[0], tw[0], ty, tr,
+                        tu, *g);
   }
   // One tile over all rows: its box ends at the last row (a box whose trailing
   // rows all lie outside the tensor copies slower).
@@ -579,8 +579,8 @@ int bq_gated_grad_quant(const void* dh_bf16, int64_t ld_dh, const void* gu_bf16,
     return launch(kern,
                   dim3(static_cast<unsigned>(ceil_div(M, 128)),
                        static_cast<unsigned>(ceil_div(N, 128))),
-                  bq::kGradThreads, bq::GradSmem::kBytes, 1, stream, th, tg, tu, M, N, qr, sr, qt, st8, d,
-                  d_status, dev.err);
+                  bq::kGradThreads, bq::GradSmem::kBytes, 1, stream, th, tg, tu, M, N, qr, sr, qt,
+                  st8, d, d_status, dev.err);
   }
   auto kern = act == BQ_GATE_SILU ? bq::gated_grad_sr_kernel<bq::kGateSilu>
                                   : bq::gated_grad_sr_kernel<bq::kGateGelu>;

@@ -1,5 +1,6 @@
 // ffn_args.cuh -- arguments and arithmetic that the int8 product and the
-// gated feed-forward kernels share (lin_swap.cuh, lin_pair.cuh).
+// gated feed-forward kernels share (lin_swap.cuh, lin_pair.cuh, gated_mx.cuh,
+// gated_grad.cuh).
 //
 // Both compute products A B^T of K-major operands of one byte per code:
 //   int8   s8 codes, exact s32 sums (tcgen05.mma kind::i8); a token's scale

@@ -524,8 +524,9 @@ int bq_act_quant_int8(const void *x_bf16, int64_t M, int64_t K, int64_t ldx, voi
  * The _epilogue form: y = bf16(act(alpha a_scale b_scale sum + bias) + residual)
  * with bq_epilogue's options except the quantized output (BQ_ERR_INVALID), and
  * bq_batch (its scale strides step the fp32 scales: bytes, multiples of 4 for
- * a_scale, of 16 for b_scale).  It needs no workspace.  Stream order as the GEMMs above: b may be read early
- * (a_scale, b_scale, bias and residual are not).
+ * a_scale, of 16 for b_scale).  It needs no workspace.  Stream order as the
+ * GEMMs above: b may be read early (a_scale, b_scale, bias and residual are not).
+ * M, N <= 0x7FFFFE00 (here and in bq_gemm_gated).
  * Schedules (bq_gemm_config): swap_ab 1: block_n 32, 64 or 128 activation rows
  * per tile, split_k 1 .. 8 CTAs of a cluster (split_mode AUTO or CLUSTER);
  * swap_ab 0: 256 x 256 tiles on pairs of SMs (cta_pair 2, block_n 256), unsplit.
