@@ -94,9 +94,60 @@ __device__ __forceinline__ float gate_act(float g, int act) {
   return act == kGateSilu ? silu(g) : gelu_gate(g);
 }
 
+// Two fp32 values in one register pair: one instruction for both, each rounded as
+// the single operation is.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2_bf16(uint32_t w) {  // of two bf16
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ void f2_get(F2 v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// gelu_cdf of two values.
+__device__ __forceinline__ F2 gelu_cdf2(F2 g, F2 &e) {
+  constexpr float kSlope = 0.3275911f * 0.70710678118654752f;
+  float g0, g1, e0, e1, h0, h1;
+  f2_get(g, g0, g1);
+  const F2 k = f2(rcp_fast(fmaf(kSlope, fabsf(g0), 1.0f)), rcp_fast(fmaf(kSlope, fabsf(g1), 1.0f)));
+  F2 poly = fma2(k, f2(0.5307027145f, 0.5307027145f), f2(-0.7265760135f, -0.7265760135f));
+  poly = fma2(k, poly, f2(0.7107068705f, 0.7107068705f));
+  poly = fma2(k, poly, f2(-0.142248368f, -0.142248368f));
+  poly = fma2(k, poly, f2(0.127414796f, 0.127414796f));  // the polynomial's half
+  f2_get(mul2(mul2(g, f2(-0.5f * kLog2e, -0.5f * kLog2e)), g), e0, e1);
+  e = f2(exp2_fast(e0), exp2_fast(e1));
+  f2_get(mul2(mul2(k, poly), e), h0, h1);
+  return f2(g0 >= 0.0f ? 1.0f - h0 : h0, g1 >= 0.0f ? 1.0f - h1 : h1);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ uint32_t pack_bf16(F2 v) {
+  float lo, hi;
+  f2_get(v, lo, hi);
+  return pack_bf16(lo, hi);
 }
 
 }  // namespace bq

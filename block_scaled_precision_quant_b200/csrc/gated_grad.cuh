@@ -32,6 +32,25 @@ __device__ __forceinline__ void gate_grad(float dh, float g, float u, float &dg,
   }
 }
 
+// The same for two elements.
+template <int ACT>
+__device__ __forceinline__ void gate_grad2(F2 dh, F2 g, F2 u, F2 &dg, F2 &du) {
+  if constexpr (ACT == kGateSilu) {
+    float a, b;
+    f2_get(mul2(g, f2(-kLog2e, -kLog2e)), a, b);
+    f2_get(add2(f2(exp2_fast(a), exp2_fast(b)), f2(1.0f, 1.0f)), a, b);
+    const F2 s = f2(rcp_fast(a), rcp_fast(b)), t = mul2(g, s);
+    du = mul2(dh, t);
+    dg = mul2(mul2(dh, u), fma2(t, fma2(s, f2(-1.0f, -1.0f), f2(1.0f, 1.0f)), s));
+  } else {
+    F2 e;
+    const F2 p = gelu_cdf2(g, e);
+    du = mul2(dh, mul2(g, p));
+    constexpr float kDensity = 0.39894228040143268f;  // 1 / sqrt(2 pi)
+    dg = mul2(mul2(dh, u), fma2(mul2(g, f2(kDensity, kDensity)), e, p));
+  }
+}
+
 // Both quantizations of one warp tile: 32 rows x 64 columns of d, lane l holding
 // row r0 + l in w (column 2 i in the low half of word i), zeros where there is
 // nothing.  c0: the tile's first column in d (C = 2 F columns), ncols = 32 or 64
@@ -294,13 +313,10 @@ __global__ void __launch_bounds__(kGradThreads, 2) gated_grad_rne_kernel(
       uint32_t og[4], ou[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float dg[2], du[2];
-        gate_grad<ACT>(__uint_as_float(h4[j] << 16), __uint_as_float(g4[j] << 16),
-                       __uint_as_float(u4[j] << 16), dg[0], du[0]);
-        gate_grad<ACT>(__uint_as_float(h4[j] & 0xFFFF0000u), __uint_as_float(g4[j] & 0xFFFF0000u),
-                       __uint_as_float(u4[j] & 0xFFFF0000u), dg[1], du[1]);
-        og[j] = pack_bf16(dg[0], dg[1]);
-        ou[j] = pack_bf16(du[0], du[1]);
+        F2 dg, du;
+        gate_grad2<ACT>(f2_bf16(h4[j]), f2_bf16(g4[j]), f2_bf16(u4[j]), dg, du);
+        og[j] = pack_bf16(dg);
+        ou[j] = pack_bf16(du);
       }
       const int r = r1 + 32 * k;
       __syncwarp();  // the row has been read
@@ -334,14 +350,16 @@ __global__ void __launch_bounds__(kGradThreads, 2) gated_grad_rne_kernel(
       bad |= mx >= 0x7F80u ? 1u : 0u;
       mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
       const int e = mx_exponent_e5m2(mx);
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const float inv1 = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const F2 inv = f2(inv1, inv1);
       uint32_t codes[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        codes[i] = e5m2x4(__fmul_rn(__uint_as_float(w[2 * i] << 16), inv),
-                          __fmul_rn(__uint_as_float(w[2 * i] & 0xFFFF0000u), inv),
-                          __fmul_rn(__uint_as_float(w[2 * i + 1] << 16), inv),
-                          __fmul_rn(__uint_as_float(w[2 * i + 1] & 0xFFFF0000u), inv));
+      for (int i = 0; i < 4; ++i) {
+        float c[4];
+        f2_get(mul2(f2_bf16(w[2 * i]), inv), c[0], c[1]);
+        f2_get(mul2(f2_bf16(w[2 * i + 1]), inv), c[2], c[3]);
+        codes[i] = e5m2x4(c[0], c[1], c[2], c[3]);
+      }
       if (r < nrows && 16 * j < ncols)
         *reinterpret_cast<uint4 *>(q_row + (b0 + r) * C + half * F + c0 + 16 * j) =
             make_uint4(codes[0], codes[1], codes[2], codes[3]);
@@ -369,16 +387,13 @@ __global__ void __launch_bounds__(kGradThreads, 2) gated_grad_rne_kernel(
     uint8_t *sft = sm + GradSmem::kOffSft + (half * 128 + 2 * p) * 4 + rg;
     sft[0] = static_cast<uint8_t>(ok ? e0 + 127 : 127);
     sft[4] = static_cast<uint8_t>(ok ? e1 + 127 : 127);
-    const float inv0 = __uint_as_float(static_cast<uint32_t>(127 - e0) << 23);
-    const float inv1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
+    const F2 inv = f2(__uint_as_float(static_cast<uint32_t>(127 - e0) << 23),
+                      __uint_as_float(static_cast<uint32_t>(127 - e1) << 23));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {  // rows 4 j .. 4 j + 3
       float lo[4], hi[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        lo[t] = __fmul_rn(__uint_as_float(w[4 * j + t] << 16), inv0);
-        hi[t] = __fmul_rn(__uint_as_float(w[4 * j + t] & 0xFFFF0000u), inv1);
-      }
+      for (int t = 0; t < 4; ++t) f2_get(mul2(f2_bf16(w[4 * j + t]), inv), lo[t], hi[t]);
       out[0][j] = e5m2x4(lo[0], lo[1], lo[2], lo[3]);
       out[1][j] = e5m2x4(hi[0], hi[1], hi[2], hi[3]);
     }
