@@ -140,6 +140,17 @@ __device__ __forceinline__ F2 gelu_cdf2(F2 g, F2 &e) {
   return f2(g0 >= 0.0f ? 1.0f - h0 : h0, g1 >= 0.0f ? 1.0f - h1 : h1);
 }
 
+__device__ __forceinline__ F2 gelu_gate2(F2 g) {
+  F2 e;
+  return mul2(g, gelu_cdf2(g, e));
+}
+__device__ __forceinline__ F2 silu2(F2 g) {
+  float a, b;
+  f2_get(mul2(g, f2(-kLog2e, -kLog2e)), a, b);
+  f2_get(add2(f2(exp2_fast(a), exp2_fast(b)), f2(1.0f, 1.0f)), a, b);
+  return mul2(g, f2(rcp_fast(a), rcp_fast(b)));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&p);

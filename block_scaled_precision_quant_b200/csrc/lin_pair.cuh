@@ -136,13 +136,13 @@ __device__ __forceinline__ void gated_out(const FfnArgs &a, const OutSlot &out,
   }
   if (a.act == kGateSilu) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) g[j] = silu(g[j]) * up[j];
+    for (int j = 0; j < 16; ++j)
+      o[j] = pack_bf16(mul2(silu2(f2(g[2 * j], g[2 * j + 1])), f2(up[2 * j], up[2 * j + 1])));
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) g[j] = gelu_gate(g[j]) * up[j];
+    for (int j = 0; j < 16; ++j)
+      o[j] = pack_bf16(mul2(gelu_gate2(f2(g[2 * j], g[2 * j + 1])), f2(up[2 * j], up[2 * j + 1])));
   }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) o[j] = pack_bf16(g[2 * j], g[2 * j + 1]);
   if (a.q_out) quant_out_row32(a, 0, m0 + out.row, q0, o);
   if (a.y) store_chunk(out, tm_y, q0, m0, a.M, 0, o);
 }
@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
           }
           if (a.act == 1) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = gelu_gate(f[j]);
+            for (int j = 0; j < 16; ++j)
+              f2_get(gelu_gate2(f2(f[2 * j], f[2 * j + 1])), f[2 * j], f[2 * j + 1]);
           }
           uint32_t o[16];
           if constexpr (RES) {
