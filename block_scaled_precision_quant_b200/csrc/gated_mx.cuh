@@ -10,14 +10,15 @@
 // each, three to a K block.
 //
 // Bound by the tensor pipe, MMAs and copies together: 4096 x 6144 x 1536 with the
-// projections kept takes 78 us (2.0 PFLOP/s), 0.46 us a K block where int8 tiles of
-// the same size take 0.33.
+// projections kept takes 77 us (2.0 PFLOP/s; 68 without), 0.42 us a K block where
+// int8 tiles of the same size take 0.34, and some 1.2 us a tile to hand the sums over.
 //
 // Tried on 4096 x 6144 x 1536 and left: 96 outputs a tile and two sets of sums,
 // with the scales laid out for any 32-row offset by four warps - stores to TMEM by
 // those warps (tcgen05.st) wait for the MMAs' own traffic (107 us), larger copies
 // (.128x256b) need a ring of replicated scales deeper than shared memory has room
-// for (89 us).
+// for (89 us).  MMAs of N = 128 for each weight, which would let one weight's first
+// sums overlap the epilogue, are slower themselves (0.51 us a K block against 0.42).
 #pragma once
 
 #include "lin_pair.cuh"
