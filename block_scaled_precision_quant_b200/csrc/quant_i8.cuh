@@ -14,6 +14,11 @@
 //
 // Reads 2 bytes and writes 1 an element; HBM bounds it: 8192 x 8192 32.2 us, 6.2 TB/s,
 // 97 % of the copy rate.
+//
+// The next kernel is not let go before this one has ended: it may be a product whose
+// weight these codes are, and products read their weights ahead.  (An early start gains
+// a product that follows 0.6 us of 6.4 to 11.5; this kernel alone takes 1.3 us for
+// 41 x 1536 without it, 1.5 with it.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -50,7 +55,6 @@ __global__ void __launch_bounds__(256) i8_quant_warp_kernel(const __nv_bfloat16 
   const int lane = threadIdx.x & 31;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   griddep_wait();
-  griddep_launch_dependents();
   if (m >= M) return;  // whole warps leave
   const uint4 *src = reinterpret_cast<const uint4 *>(x + m * ldx);
   const int nv = static_cast<int>(K / 8);
@@ -88,7 +92,6 @@ __global__ void __launch_bounds__(256) i8_quant_kernel(const __nv_bfloat16 *__re
                                                        int *__restrict__ status) {
   __shared__ uint32_t part[8];
   griddep_wait();
-  griddep_launch_dependents();
   const int64_t m = blockIdx.x;
   const uint4 *src = reinterpret_cast<const uint4 *>(x + m * ldx);
   const int64_t nv = K / 8;

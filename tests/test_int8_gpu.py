@@ -66,6 +66,29 @@ def test_quant_small_zero_and_large_rows():
     assert int(q[0].abs().max()) == 0 and int(q[1].min()) == 127
 
 
+@pytest.mark.parametrize("M,N,K", [(41, 4608, 1536), (300, 8192, 4096)])
+def test_weight_quantized_right_before_the_product(M, N, K):
+    """The weight's codes come last before the product, into buffers that held others."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+    ws = [torch.randn((N, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    want = []
+    for w in ws:
+        q, s = bq.act_quant_int8(x)
+        b, sb = bq.act_quant_int8(w)
+        torch.cuda.synchronize()
+        want.append(bq.gemm_int8_int8(q, s, b, sb, M, N, K))
+    torch.cuda.synchronize()
+    b, sb = torch.zeros_like(b), torch.zeros_like(sb)
+    got = []
+    for w in ws * 4:
+        q, s = bq.act_quant_int8(x)
+        bq.act_quant_int8(w, b, sb)
+        got.append(bq.gemm_int8_int8(q, s, b, sb, M, N, K))
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 3])
+
+
 @pytest.mark.parametrize("M", [45, 605])
 def test_quant_row_stride_outputs_and_status(M):
     wide = rows(M, 200, 3)
