@@ -588,41 +588,31 @@ def gemm_e5m2_mxfp8(a_e5m2, a_sf, b_e4m3, b_sf, M, N, K, **kw):
 
 # -------------------------------------------- int8 and gated feed-forward ----
 
-# (Outputs come from torch.empty_strided: it returns a microsecond sooner than
-# torch.empty, a tenth of a small call.)
-
-def _here(torch, *ts):
-    """The current stream of the current device, on which the calls run and their
-    tensors live.  (The raw getters: the Stream object that
-    torch.cuda.current_stream builds costs more than a launch.)"""
-    dev = -1
-    for t in ts:
-        if t is not None:
-            d = t.get_device()
-            if d < 0:
-                raise ValueError("libbq works on CUDA tensors only")
-            if dev < 0:
-                dev = torch._C._cuda_getDevice()
-            if d != dev:
-                raise ValueError("tensors must be on the current CUDA device")
-    return torch._C._cuda_getCurrentRawStream(dev)
+_native = None
 
 
-def _need(t, dtype, numel, what):
-    if t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of at least {numel} elements")
+def _load_native():
+    """The compiled calls of these operators (csrc/torch_calls.cpp): argument checks,
+    output tensors and the library call, in a third of the time that they take
+    through ctypes, where small calls spend most of it."""
+    global _native
+    if _native is None:
+        _torch()
+        L = lib()
+        try:
+            from . import _torch_calls as m
+        except ImportError as e:
+            raise RuntimeError("the compiled calls are missing: build them with "
+                               "`python -m block_scaled_precision_quant_b200.build`") from e
+        m.init(BqError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.bq_act_quant_int8, L.bq_gemm_int8_int8_epilogue, L.bq_gemm_gated,
+            L.bq_gated_grad_quant)))
+        _native = m
+    return _native
 
 
-def _need_rows(t, rows, cols, what):
-    """bf16 [rows, cols] with unit column stride (the row stride may exceed cols)."""
-    if (t.dtype is not _torch().bfloat16 or t.shape != (rows, cols)
-            or (cols > 1 and t.stride(1) != 1)):
-        raise ValueError(f"{what} must be a bf16 [{rows}, {cols}] tensor with unit column stride")
-
-
-def _ld(t):
-    """Row stride of a 2-D tensor (one row has none of its own)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _config_at(config):
+    return None if config is None else ctypes.addressof(config)
 
 
 def ffn_plan(M, N, K, batch=1, config=None, num_sms=148, weight_kind=W_INT8,
@@ -640,24 +630,7 @@ def act_quant_int8(x, q=None, scale=None, status=None):
     """Per-row int8 quantization of a bf16 [M, K] CUDA tensor (row stride may
     exceed K): returns (q int8 [M, K], scale fp32 [M]), q * scale ~ x.  Also the
     quantizer of a weight [N, K] with one scale per output channel."""
-    torch = _torch()
-    stream = _here(torch, x, q, scale, status)
-    if x.dtype is not torch.bfloat16 or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError("x must be a bf16 [M, K] tensor with unit column stride")
-    M, K = x.shape
-    if q is None:
-        q = torch.empty_strided((M, K), (K, 1), dtype=torch.int8, device=x.device)
-    else:
-        _need(q, torch.int8, M * K, "q")
-    if scale is None:
-        scale = torch.empty_strided((M,), (1,), dtype=torch.float32, device=x.device)
-    else:
-        _need(scale, torch.float32, M, "scale")
-    st = lib().bq_act_quant_int8(x.data_ptr(), M, K, _ld(x), q.data_ptr(), scale.data_ptr(),
-                                 None if status is None else status.data_ptr(), stream)
-    if st:
-        raise BqError(st, "bq_act_quant_int8")
-    return q, scale
+    return (_native or _load_native()).act_quant_int8(x, q, scale, status)
 
 
 def gemm_int8_int8(a_q, a_scale, b, b_scale, M, N, K, y=None, bias=None, residual=None, alpha=1.0,
@@ -666,55 +639,12 @@ def gemm_int8_int8(a_q, a_scale, b, b_scale, M, N, K, y=None, bias=None, residua
     int8 codes a_q [.., M, K] and b [.., N, K] with fp32 scales per token and per
     output channel (act_quant_int8).  batch: as in gemm; its scale strides
     step the fp32 scales.  config: GemmConfig or None (auto)."""
-    torch = _torch()
-    stream = _here(torch, a_q, a_scale, b, b_scale, y, bias, residual)
-    count, sa, ssa, sb, ssb, sy, sr = 1, 0, 0, 0, 0, 0, 0
     if batch is not None:
-        count = int(batch["count"])
-        sa, ssa, sb, ssb, sy, sr = (int(batch.get(k, 0)) for k in (
-            "stride_a", "stride_a_sf", "stride_b", "stride_b_sf", "stride_y", "stride_res"))
-    more = max(count - 1, 0) if M and N else 0
-    _need(a_q, torch.int8, M * K + more * sa, "a_q")
-    _need(b, torch.int8, N * K + more * sb, "b")
-    _need(a_scale, torch.float32, M + more * (ssa // 4), "a_scale")
-    _need(b_scale, torch.float32, N + more * (ssb // 4), "b_scale")
-    if y is None:
-        if batch is None:
-            y = torch.empty_strided((M, N), (N, 1), dtype=torch.bfloat16, device=a_q.device)
-        else:
-            y = torch.empty((count, M, N), dtype=torch.bfloat16, device=a_q.device)
-    else:
-        _need(y, torch.bfloat16, M * N + more * (sy // 2), "y")
-    L = lib()
-    if (bias is None and residual is None and alpha == 1.0 and act == BQ_ACT_NONE
-            and batch is None and config is None):
-        st = L.bq_gemm_int8_int8(a_q.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
-                                 b_scale.data_ptr(), M, N, K, y.data_ptr(), stream)
-        if st:
-            raise BqError(st, "bq_gemm_int8_int8")
-        return y
-    epi = Epilogue(None, None, 0, alpha, act, None, None)
-    if bias is not None:
-        _need(bias, torch.bfloat16, N, "bias")
-        epi.bias = bias.data_ptr()
-    if residual is not None:
-        if batch is None:
-            _need_rows(residual, M, N, "residual")
-            epi.ld_residual = _ld(residual)
-        else:
-            if (residual.dtype is not torch.bfloat16 or residual.dim() < 2
-                    or residual.stride(-1) != 1):
-                raise ValueError("residual must be bf16 with unit column stride")
-            epi.ld_residual = residual.stride(-2)
-        epi.residual = residual.data_ptr()
-    bt = None if batch is None else ctypes.byref(Batch(count, sa, ssa, sb, ssb, sy, sr))
-    st = L.bq_gemm_int8_int8_epilogue(
-        a_q.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), M, N, K,
-        y.data_ptr(), ctypes.byref(epi), bt, None if config is None else ctypes.byref(config),
-        stream)
-    if st:
-        raise BqError(st, "bq_gemm_int8_int8_epilogue")
-    return y
+        batch = (int(batch["count"]), *(int(batch.get(k, 0)) for k in (
+            "stride_a", "stride_a_sf", "stride_b", "stride_b_sf", "stride_y", "stride_res")))
+    return (_native or _load_native()).gemm_int8_int8(
+        a_q, a_scale, b, b_scale, M, N, K, y, bias, residual, alpha, act, batch,
+        _config_at(config))
 
 
 def gemm_gated(weight_kind, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, M, N, K, y=None,
@@ -729,56 +659,12 @@ def gemm_gated(weight_kind, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, M, N, K, y=
     projection (E4M3 codes and MMA-layout scales, exactly act_quant of h); no bf16
     h is written when write_y is False.  Returns h, or a tuple (h or None, [q, sf],
     [gu]) when quantize_out or keep_projections ask for more."""
-    torch = _torch()
-    stream = _here(torch, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, y, gu, q_out, sf_out)
-    if not write_y and not quantize_out:
-        raise ValueError("write_y=False needs quantize_out=True")
-    if weight_kind == W_INT8:
-        code, scale, na, nw, nws = torch.int8, torch.float32, M, N * K, N
-    else:
-        code = scale = torch.uint8
-        ka = -(-K // 128) * 512
-        na, nws = -(-M // 128) * ka, -(-N // 128) * ka
-        nw = N * K // 2 if weight_kind == W_MXFP4 else N * K
-    _need(a_q, code, M * K, "a_q")
-    _need(a_sf, scale, na, "a_sf")
-    _need(b_gate, code, nw, "b_gate")
-    _need(gate_sf, scale, nws, "gate_sf")
-    _need(b_up, code, nw, "b_up")
-    _need(up_sf, scale, nws, "up_sf")
-    epi = GatedEpilogue(alpha, act, None, None, None)
-    if not write_y:
-        y = None
-    elif y is None:
-        y = torch.empty_strided((M, N), (N, 1), dtype=torch.bfloat16, device=a_q.device)
-    else:
-        _need(y, torch.bfloat16, M * N, "y")
-    if gu is not None:
-        _need(gu, torch.bfloat16, 2 * M * N, "gu")
-    elif keep_projections:
-        gu = torch.empty_strided((M, 2 * N), (2 * N, 1), dtype=torch.bfloat16, device=a_q.device)
-    if gu is not None:
-        epi.gu_out = gu.data_ptr()
-    if quantize_out:
-        nsf = -(-M // 128) * -(-N // 128) * 512
-        if q_out is None:
-            q_out = torch.empty_strided((M, N), (N, 1), dtype=torch.uint8, device=a_q.device)
-        else:
-            _need(q_out, torch.uint8, M * N, "q_out")
-        if sf_out is None:
-            sf_out = torch.empty_strided((max(nsf, 1),), (1,), dtype=torch.uint8, device=a_q.device)
-        else:
-            _need(sf_out, torch.uint8, nsf, "sf_out")
-        epi.q_out, epi.sf_out = q_out.data_ptr(), sf_out.data_ptr()
-    st = lib().bq_gemm_gated(
-        weight_kind, a_q.data_ptr(), a_sf.data_ptr(), b_gate.data_ptr(), gate_sf.data_ptr(),
-        b_up.data_ptr(), up_sf.data_ptr(), M, N, K, None if y is None else y.data_ptr(),
-        ctypes.byref(epi), None if config is None else ctypes.byref(config), stream)
-    if st:
-        raise BqError(st, "bq_gemm_gated")
-    if not quantize_out and gu is None:
+    y, q, sf, gu = (_native or _load_native()).gemm_gated(
+        weight_kind, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, M, N, K, y, act, alpha,
+        keep_projections, gu, quantize_out, write_y, q_out, sf_out, _config_at(config))
+    if q is None and gu is None:
         return y
-    return (y,) + ((q_out, sf_out) if quantize_out else ()) + ((gu,) if gu is not None else ())
+    return (y,) + ((q, sf) if q is not None else ()) + ((gu,) if gu is not None else ())
 
 
 def gated_grad_quant(dh, gu, act=BQ_GATE_SILU, stochastic=False, seed=0, out=None, d=None,
@@ -787,39 +673,10 @@ def gated_grad_quant(dh, gu, act=BQ_GATE_SILU, stochastic=False, seed=0, out=Non
     from dh bf16 [M, N] and gu = [g | u] bf16 [M, 2 N], quantized to E5M2 along
     both dimensions as grad_quant_dual(d) does.  Returns (q_row [M, 2 N], sf_row, q_t
     [2 N, M], sf_t); d (bf16 [M, 2 N]) is written when given."""
-    torch = _torch()
-    q_row = sf_row = q_t = sf_t = None
-    if out is not None:
-        q_row, sf_row, q_t, sf_t = out
-    stream = _here(torch, dh, gu, q_row, sf_row, q_t, sf_t, d, status)
-    if dh.dim() != 2:
-        raise ValueError("dh must be a bf16 [M, N] tensor")
-    M, N = dh.shape
-    _need_rows(dh, M, N, "dh")
-    _need_rows(gu, M, 2 * N, "gu")
-    n_row = max(-(-M // 128) * -(-2 * N // 128) * 512, 1)  # both scale buffers have as many atoms
-    if out is None:
-        u8 = torch.uint8
-        dev = dh.device
-        q_row = torch.empty_strided((M, 2 * N), (2 * N, 1), dtype=u8, device=dev)
-        sf_row = torch.empty_strided((n_row,), (1,), dtype=u8, device=dev)
-        q_t = torch.empty_strided((2 * N, M), (M, 1), dtype=u8, device=dev)
-        sf_t = torch.empty_strided((n_row,), (1,), dtype=u8, device=dev)
-    else:
-        _need(q_row, torch.uint8, 2 * M * N, "q_row")
-        _need(q_t, torch.uint8, 2 * M * N, "q_t")
-        _need(sf_row, torch.uint8, n_row, "sf_row")
-        _need(sf_t, torch.uint8, n_row, "sf_t")
-    if d is not None:
-        _need(d, torch.bfloat16, 2 * M * N, "d")
-    st = lib().bq_gated_grad_quant(
-        dh.data_ptr(), _ld(dh), gu.data_ptr(), _ld(gu), M, N, act,
-        BQ_ROUND_STOCHASTIC if stochastic else BQ_ROUND_NEAREST, int(seed) & (2 ** 64 - 1),
-        q_row.data_ptr(), sf_row.data_ptr(), q_t.data_ptr(), sf_t.data_ptr(),
-        None if d is None else d.data_ptr(), None if status is None else status.data_ptr(), stream)
-    if st:
-        raise BqError(st, "bq_gated_grad_quant")
-    return q_row, sf_row, q_t, sf_t
+    q_row, sf_row, q_t, sf_t = (None,) * 4 if out is None else out
+    return (_native or _load_native()).gated_grad_quant(
+        dh, gu, act, BQ_ROUND_STOCHASTIC if stochastic else BQ_ROUND_NEAREST, seed, q_row, sf_row,
+        q_t, sf_t, d, status)
 
 
 config = _config

@@ -1,17 +1,22 @@
 """Build libbq.so (the CUDA library behind include/bq.h) in-tree with nvcc for
-sm_100a.  Usage: python -m block_scaled_precision_quant_b200.build [--force]"""
+sm_100a, and, where torch is installed, the binding's compiled calls on torch tensors
+(_torch_calls.so).  Usage: python -m block_scaled_precision_quant_b200.build [--force]"""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbq.so")
+CALLS = os.path.join(PKG, "_torch_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -38,14 +43,43 @@ def nvcc() -> str:
     return "nvcc"
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def current(built: str, files) -> bool:
+    if not os.path.exists(built):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in deps())
+    t = os.path.getmtime(built)
+    return all(os.path.getmtime(d) <= t for d in files)
+
+
+def up_to_date() -> bool:
+    return current(LIB, deps())
+
+
+def build_calls(force: bool = False):
+    """The extension module of csrc/torch_calls.cpp (g++), or None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    if not force and current(CALLS, [CALLS_SOURCE, os.path.join(INCLUDE, "bq.h")]):
+        return CALLS
+    torch_dir = os.path.dirname(spec.origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden", "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(cuda, "include"), CALLS_SOURCE,
+           "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_cuda", "-ltorch_python", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed building _torch_calls.so")
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_calls(force)
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
