@@ -9,7 +9,7 @@
 // amax = A 2^j, X and A below 2^8, any other n is at least 1 / (2 A) of a unit
 // of 2^(i - j) away from a tie, that is 2^-17 relative.  Rounding y to 18
 // bits moves it by at most 2^-18 relative: ties land on themselves, nothing
-// else does.  Then the conversion's own round to nearest even decides.  The
+// else does.  Then an addition's own round to nearest even decides.  The
 // floor of amax is a power of two so that A stays short.
 //
 // Reads 2 bytes and writes 1 an element; HBM bounds it: 8192 x 8192 32.2 us, 6.2 TB/s,
@@ -25,20 +25,28 @@
 #include <stdint.h>
 
 #include "bq_ptx.cuh"
+#include "f32x2.cuh"
 #include "mx_quant.cuh"
 
 namespace bq {
 
-// Int8 code (low byte) of the bf16 value whose fp32 bits are `bits`.
-__device__ __forceinline__ int i8_code(uint32_t bits, float c) {
-  const uint32_t y = __float_as_uint(__fmul_rn(__uint_as_float(bits), c));
-  return __float2int_rn(__uint_as_float((y + 32u) & ~63u));
+// Codes of two bf16 values in the low bytes of lo and hi: y rounded to 18 bits (the
+// product with 2^6 + 1 carries the rest of y beyond the 24), then to an integer by
+// adding 1.5 2^23, whose low byte is the code.
+__device__ __forceinline__ void i8_codes2(uint32_t w, F2 c, uint32_t &lo, uint32_t &hi) {
+  const F2 y = mul2(f2_bf16(w), c), p = mul2(y, f2(65.0f, 65.0f)), minus = f2(-1.0f, -1.0f);
+  const F2 s = fma2(fma2(y, minus, p), minus, p);
+  float a, b;
+  f2_get(add2(s, f2(12582912.0f, 12582912.0f)), a, b);
+  lo = __float_as_uint(a);
+  hi = __float_as_uint(b);
 }
 
 // Four codes of two words of bf16 pairs.
-__device__ __forceinline__ uint32_t i8_codes4(uint32_t w0, uint32_t w1, float c) {
-  const int a = i8_code(w0 << 16, c), b = i8_code(w0 & 0xFFFF0000u, c);
-  const int d = i8_code(w1 << 16, c), e = i8_code(w1 & 0xFFFF0000u, c);
+__device__ __forceinline__ uint32_t i8_codes4(uint32_t w0, uint32_t w1, F2 c) {
+  uint32_t a, b, d, e;
+  i8_codes2(w0, c, a, b);
+  i8_codes2(w1, c, d, e);
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(d, e, 0x0040), 0x5410);
 }
 
@@ -72,7 +80,8 @@ __global__ void __launch_bounds__(256) i8_quant_warp_kernel(const __nv_bfloat16 
   }
   mx = __reduce_max_sync(0xFFFFFFFFu, mx);
   const float amax = fmaxf(__uint_as_float(mx << 16), 0x1p-64f);
-  const float c = __fdiv_rn(127.0f, amax);
+  const float c1 = __fdiv_rn(127.0f, amax);
+  const F2 c = f2(c1, c1);
   if (lane == 0) {
     scale[m] = __fdiv_rn(amax, 127.0f);
     if (mx >= 0x7F80u && status) atomicOr(status, 1);
@@ -107,7 +116,8 @@ __global__ void __launch_bounds__(256) i8_quant_kernel(const __nv_bfloat16 *__re
 #pragma unroll
   for (int i = 0; i < 8; ++i) mx = max(mx, part[i]);
   const float amax = fmaxf(__uint_as_float(mx << 16), 0x1p-64f);
-  const float c = __fdiv_rn(127.0f, amax);
+  const float c1 = __fdiv_rn(127.0f, amax);
+  const F2 c = f2(c1, c1);
   if (threadIdx.x == 0) {
     scale[m] = __fdiv_rn(amax, 127.0f);
     if (mx >= 0x7F80u && status) atomicOr(status, 1);
