@@ -93,7 +93,10 @@ __global__ void __launch_bounds__(256) i8_quant_warp_kernel(const __nv_bfloat16 
       dst[lane + 32 * i] = make_uint2(i8_codes4(t[i].x, t[i].y, c), i8_codes4(t[i].z, t[i].w, c));
 }
 
-// One block per row; the row is read twice (the second time from the caches).
+// One block per row.  Each thread keeps its first kI8BlockVecs 16-byte pieces (rows of
+// up to 8192 values whole); the rest of a longer row is read twice, the second time
+// from the caches.
+constexpr int kI8BlockVecs = 4;
 __global__ void __launch_bounds__(256) i8_quant_kernel(const __nv_bfloat16 *__restrict__ x,
                                                        int64_t M, int64_t K, int64_t ldx,
                                                        uint8_t *__restrict__ q,
@@ -104,10 +107,21 @@ __global__ void __launch_bounds__(256) i8_quant_kernel(const __nv_bfloat16 *__re
   const int64_t m = blockIdx.x;
   const uint4 *src = reinterpret_cast<const uint4 *>(x + m * ldx);
   const int64_t nv = K / 8;
+  uint4 t[kI8BlockVecs];
   uint32_t mx = 0, bad = 0;
-  for (int64_t i = threadIdx.x; i < nv; i += 256) {
-    const uint4 t = __ldg(src + i);
-    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+  for (int i = 0; i < kI8BlockVecs; ++i) {
+    t[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x + 256 * i < nv) t[i] = __ldg(src + threadIdx.x + 256 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < kI8BlockVecs; ++i) {
+    const uint32_t w[4] = {t[i].x, t[i].y, t[i].z, t[i].w};
+    mx = max(mx, bf16_amax_bits(w, bad));
+  }
+  for (int64_t i = threadIdx.x + 256 * kI8BlockVecs; i < nv; i += 256) {
+    const uint4 v = __ldg(src + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     mx = max(mx, bf16_amax_bits(w, bad));
   }
   mx = __reduce_max_sync(0xFFFFFFFFu, mx);
@@ -123,9 +137,14 @@ __global__ void __launch_bounds__(256) i8_quant_kernel(const __nv_bfloat16 *__re
     if (mx >= 0x7F80u && status) atomicOr(status, 1);
   }
   uint2 *dst = reinterpret_cast<uint2 *>(q + m * K);
-  for (int64_t i = threadIdx.x; i < nv; i += 256) {
-    const uint4 t = __ldg(src + i);
-    dst[i] = make_uint2(i8_codes4(t.x, t.y, c), i8_codes4(t.z, t.w, c));
+#pragma unroll
+  for (int i = 0; i < kI8BlockVecs; ++i)
+    if (threadIdx.x + 256 * i < nv)
+      dst[threadIdx.x + 256 * i] =
+          make_uint2(i8_codes4(t[i].x, t[i].y, c), i8_codes4(t[i].z, t[i].w, c));
+  for (int64_t i = threadIdx.x + 256 * kI8BlockVecs; i < nv; i += 256) {
+    const uint4 v = __ldg(src + i);
+    dst[i] = make_uint2(i8_codes4(v.x, v.y, c), i8_codes4(v.z, v.w, c));
   }
 }
 
