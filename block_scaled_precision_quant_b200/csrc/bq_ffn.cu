@@ -439,14 +439,16 @@ int bq_act_quant_int8(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, voi
   Device dev;
   const int st = bqh::current_device(&dev);
   if (st != BQ_OK || M == 0) return st;
-  // Many short rows get a warp each (quant_i8.cuh; 600 x 2048: 2.5 us with blocks, 2.3
-  // with warps; of longer rows it takes more: 2048 x 4096: 6.0 and 7.1, 8192 x 4096: 24.2
-  // and 18.7).
-  const bool warps = K <= 2048 ? M >= 4 * dev.num_sms : K <= 4096 && M >= 32 * dev.num_sms;
-  return launch(!warps      ? bq::i8_quant_kernel
-                : K <= 2048 ? bq::i8_quant_warp_kernel<8>
-                            : bq::i8_quant_warp_kernel<16>,
-                dim3(static_cast<unsigned>(warps ? ceil_div(M, 8) : M)), 256, 0, 1, stream,
+  // Many short rows get a warp each (quant_i8.cuh): 200 x 2048 takes 1.6 us with blocks and
+  // 1.9 with warps, 600 x 2048 2.4 and 2.0; of longer rows it takes more: 1200 x 3584 3.7
+  // and 4.0, 2048 x 4096 5.9 and 4.5.
+  const bool warps = M >= (K <= 2048 ? 4 : 10) * dev.num_sms && K <= 4096;
+  const bool small = !warps && K <= 6144 && M >= 3 * dev.num_sms;  // blocks of 128
+  return launch(warps   ? K <= 2048 ? bq::i8_quant_warp_kernel<8> : bq::i8_quant_warp_kernel<16>
+                : small ? bq::i8_quant_kernel<128, 8>
+                        : bq::i8_quant_kernel<256, 4>,
+                dim3(static_cast<unsigned>(warps ? ceil_div(M, 8) : M)), small ? 128 : 256, 0, 1,
+                stream,
                 static_cast<const __nv_bfloat16*>(x_bf16), M, K, ldx,
                 static_cast<uint8_t*>(q_s8), scale, d_status);
 }

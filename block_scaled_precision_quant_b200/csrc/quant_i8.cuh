@@ -12,8 +12,8 @@
 // else does.  Then an addition's own round to nearest even decides.  The
 // floor of amax is a power of two so that A stays short.
 //
-// Reads 2 bytes and writes 1 an element; HBM bounds it: 8192 x 8192 32.2 us, 6.2 TB/s,
-// 97 % of the copy rate.
+// Reads 2 bytes and writes 1 an element; HBM bounds it: 8192 x 8192 31.1 us, 6.5 TB/s,
+// the copy rate.
 //
 // The next kernel is not let go before this one has ended: it may be a product whose
 // weight these codes are, and products read their weights ahead.  (An early start gains
@@ -52,8 +52,8 @@ __device__ __forceinline__ uint32_t i8_codes4(uint32_t w0, uint32_t w1, F2 c) {
 
 // One warp per row of up to 256 VECS values, which stay in its registers (VECS
 // 16-byte pieces a lane).  Many short rows want it: a block to a row leaves most
-// of its threads idle (8192 x 256: 9.1 us, 3.6 with a warp each; 8192 x 2048: 14.5
-// and 9.7; but 41 x 1536: 1.5 and 2.0, so few rows keep their blocks).
+// of its threads idle (8192 x 256: 13.5 us, 3.6 with a warp each; 8192 x 2048: 18.7
+// and 9.5; but 41 x 1536: 1.26 and 1.73, so few rows keep their blocks).
 template <int kI8WarpVecs>
 __global__ void __launch_bounds__(256) i8_quant_warp_kernel(const __nv_bfloat16 *__restrict__ x,
                                                             int64_t M, int64_t K, int64_t ldx,
@@ -93,33 +93,35 @@ __global__ void __launch_bounds__(256) i8_quant_warp_kernel(const __nv_bfloat16 
       dst[lane + 32 * i] = make_uint2(i8_codes4(t[i].x, t[i].y, c), i8_codes4(t[i].z, t[i].w, c));
 }
 
-// One block per row.  Each thread keeps its first kI8BlockVecs 16-byte pieces (rows of
-// up to 8192 values whole); the rest of a longer row is read twice, the second time
-// from the caches.
-constexpr int kI8BlockVecs = 4;
-__global__ void __launch_bounds__(256) i8_quant_kernel(const __nv_bfloat16 *__restrict__ x,
-                                                       int64_t M, int64_t K, int64_t ldx,
-                                                       uint8_t *__restrict__ q,
-                                                       float *__restrict__ scale,
-                                                       int *__restrict__ status) {
-  __shared__ uint32_t part[8];
+// One block of THREADS per row.  Each thread keeps its first VECS 16-byte pieces; the
+// rest of a longer row is read twice, the second time from the caches.  256 threads
+// of 4 pieces suit long rows, 128 of 8 many middling ones (8192 x 4112: 23.7 and
+// 19.0 us, 600 x 4096: 2.6 and 2.45; 200 x 2048: 1.67 and 1.71, 8192 x 8192: 31.1
+// and 31.9).
+template <int THREADS, int VECS>
+__global__ void __launch_bounds__(THREADS) i8_quant_kernel(const __nv_bfloat16 *__restrict__ x,
+                                                           int64_t M, int64_t K, int64_t ldx,
+                                                           uint8_t *__restrict__ q,
+                                                           float *__restrict__ scale,
+                                                           int *__restrict__ status) {
+  __shared__ uint32_t part[THREADS / 32];
   griddep_wait();
   const int64_t m = blockIdx.x;
   const uint4 *src = reinterpret_cast<const uint4 *>(x + m * ldx);
   const int64_t nv = K / 8;
-  uint4 t[kI8BlockVecs];
+  uint4 t[VECS];
   uint32_t mx = 0, bad = 0;
 #pragma unroll
-  for (int i = 0; i < kI8BlockVecs; ++i) {
+  for (int i = 0; i < VECS; ++i) {
     t[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (threadIdx.x + 256 * i < nv) t[i] = __ldg(src + threadIdx.x + 256 * i);
+    if (threadIdx.x + THREADS * i < nv) t[i] = __ldg(src + threadIdx.x + THREADS * i);
   }
 #pragma unroll
-  for (int i = 0; i < kI8BlockVecs; ++i) {
+  for (int i = 0; i < VECS; ++i) {
     const uint32_t w[4] = {t[i].x, t[i].y, t[i].z, t[i].w};
     mx = max(mx, bf16_amax_bits(w, bad));
   }
-  for (int64_t i = threadIdx.x + 256 * kI8BlockVecs; i < nv; i += 256) {
+  for (int64_t i = threadIdx.x + THREADS * VECS; i < nv; i += THREADS) {
     const uint4 v = __ldg(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     mx = max(mx, bf16_amax_bits(w, bad));
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(256) i8_quant_kernel(const __nv_bfloat16 *__re
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mx;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) mx = max(mx, part[i]);
+  for (int i = 0; i < THREADS / 32; ++i) mx = max(mx, part[i]);
   const float amax = fmaxf(__uint_as_float(mx << 16), 0x1p-64f);
   const float c1 = __fdiv_rn(127.0f, amax);
   const F2 c = f2(c1, c1);
@@ -138,11 +140,11 @@ __global__ void __launch_bounds__(256) i8_quant_kernel(const __nv_bfloat16 *__re
   }
   uint2 *dst = reinterpret_cast<uint2 *>(q + m * K);
 #pragma unroll
-  for (int i = 0; i < kI8BlockVecs; ++i)
-    if (threadIdx.x + 256 * i < nv)
-      dst[threadIdx.x + 256 * i] =
+  for (int i = 0; i < VECS; ++i)
+    if (threadIdx.x + THREADS * i < nv)
+      dst[threadIdx.x + THREADS * i] =
           make_uint2(i8_codes4(t[i].x, t[i].y, c), i8_codes4(t[i].z, t[i].w, c));
-  for (int64_t i = threadIdx.x + 256 * kI8BlockVecs; i < nv; i += 256) {
+  for (int64_t i = threadIdx.x + THREADS * VECS; i < nv; i += THREADS) {
     const uint4 v = __ldg(src + i);
     dst[i] = make_uint2(i8_codes4(v.x, v.y, c), i8_codes4(v.z, v.w, c));
   }

@@ -29,7 +29,11 @@ def check_quant(x, q, s):
                                  (2500, 272),
                                  # a warp to a row: short rows and longer ones
                                  (595, 16), (1201, 2048), (700, 992), (4740, 2064),
-                                 (4737, 4096)])
+                                 (4737, 4096), (1480, 2064),
+                                 # blocks of 128: middling rows, many of them
+                                 (444, 16), (590, 1040), (600, 4096), (1481, 4112), (445, 6144),
+                                 # and of 256 again
+                                 (443, 6144), (444, 6160), (1500, 8192)])
 def test_quant_rows(M, K):
     x = rows(M, K, M + K)
     q, s = bq.act_quant_int8(x)
