@@ -153,6 +153,32 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
+  const int mt = min(BN, a.M - m0);
+  auto sums_to_smem = [&] {
+    // Sums to shared memory: a lane holds one output n, a warp store is 32
+    // consecutive n of one row m.  Every MMA that read the stages is complete.
+    const int quad = warp % 4;
+    const int row = quad * 32 + lane;
+    if (mbar_wait(tfull, 0, a.err, abort_flag, kWaitEpiFull)) {
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll
+      for (int w = 0; w < L::kWeights; ++w) {
+        uint32_t *dst = reinterpret_cast<uint32_t *>(smem + w * L::kPart) + row;
+#pragma unroll 1
+        for (int c = 0; c < BN / 32 && c * 32 < mt; ++c) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld_32x32b_x32(t_row + w * BN + c * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) dst[(c * 32 + j) * kBlockP] = v[j];
+        }
+      }
+    }
+  };
+
   const bool copier = warp == 0 || warp == 6 || (!I8 && (warp == 7 || warp == 8)) ||
                       (GATED && warp == 9);
   if (copier) {
@@ -248,35 +274,34 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
       tc_commit(drain);
       if (!mbar_wait_timed(drain, 0, a.err, kWaitDrain)) sleep_ns(200000);
     }
-  } else if (warp >= 2 && warp <= 5) {
-    // Sums to shared memory: a lane holds one output n, a warp store is 32
-    // consecutive n of one row m.  Every MMA that read the stages is complete.
-    const int quad = warp % 4;
-    const int row = quad * 32 + lane;
-    const int mt = min(BN, a.M - m0);
-    if (mbar_wait(tfull, 0, a.err, abort_flag, kWaitEpiFull)) {
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-#pragma unroll
-      for (int w = 0; w < L::kWeights; ++w) {
-        uint32_t *dst = reinterpret_cast<uint32_t *>(smem + w * L::kPart) + row;
-#pragma unroll 1
-        for (int c = 0; c < BN / 32 && c * 32 < mt; ++c) {
-          uint32_t v[32];
-          __syncwarp();
-          tmem_ld_32x32b_x32(t_row + w * BN + c * 32, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) dst[(c * 32 + j) * kBlockP] = v[j];
-        }
-      }
-    }
+  } else if (!I8 && warp >= 2 && warp <= 5) {
+    sums_to_smem();
   }
   __syncwarp();
   // The scales, bias and residual may come from the preceding kernel, which
   // may also still read or write the outputs.
   griddep_wait();
+  // What the outputs need besides the sums, fetched while those are formed (int8 41 x
+  // 1536 x 6144: 7.0 us with the scales fetched behind the exchange, 6.6 so; MX has
+  // none, and 0.15 us more in this order).
+  const int n = n0 + 4 * lane;
+  const bool nok = n < a.N;
+  float sw[2][4];
+#pragma unroll
+  for (int w = 0; w < L::kWeights; ++w) {
+    float4 s = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (I8 && nok) s = __ldg(reinterpret_cast<const float4 *>(a.sw[w] + b * a.sw_bstride + n));
+    sw[w][0] = a.alpha * s.x;
+    sw[w][1] = a.alpha * s.y;
+    sw[w][2] = a.alpha * s.z;
+    sw[w][3] = a.alpha * s.w;
+  }
+  uint2 bias = make_uint2(0u, 0u);
+  if (!GATED && a.bias && nok) bias = __ldg(reinterpret_cast<const uint2 *>(a.bias + n));
+  const int first = rank * kSwapWarps + warp;  // this warp's first row
+  float sa = I8 && first < mt ? __ldg(a.sa + b * a.sa_bstride + m0 + first) : 1.0f;
+  if (I8 && warp >= 2 && warp <= 5) sums_to_smem();
+  __syncwarp();
   tc_fence_before();
   if (S > 1)
     cluster_sync_all();
@@ -285,27 +310,14 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
 
   // ------------------------------------------------------------- outputs --
   {
-    const int mt = min(BN, a.M - m0);
-    const int n = n0 + 4 * lane;
-    const bool nok = n < a.N;
-    float sw[2][4], bias[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        sw[w][j] = (I8 && w < L::kWeights && nok)
-                       ? a.alpha * __ldg(a.sw[w] + b * a.sw_bstride + n + j)
-                       : a.alpha;
-      bias[j] = (!GATED && a.bias && nok) ? __bfloat162float(a.bias[n + j]) : 0.0f;
-    }
     const int64_t groups = a.N >> 5, katoms = (groups + 3) >> 2;
     // One row a warp and round, in code that is short: it runs once, from a cold
     // instruction cache (four rows a round, fetched together, took 0.5 to 2 us
     // longer on 41 x 1536 x 6144 split eight ways and gained nothing elsewhere).
 #pragma unroll 1
-    for (int r = rank * kSwapWarps + warp; r < mt; r += S * kSwapWarps) {
+    for (int r = first; r < mt; r += S * kSwapWarps) {
       const int m = m0 + r;
-      const float sa = I8 ? __ldg(a.sa + b * a.sa_bstride + m) : 1.0f;
+      if (I8 && r != first) sa = __ldg(a.sa + b * a.sa_bstride + m);
       float v[2][4];
 #pragma unroll
       for (int w = 0; w < L::kWeights; ++w) {
@@ -335,7 +347,8 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
         for (int j = 0; j < 4; ++j) t[j] = gate_act(v[0][j], a.act) * v[1][j];
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) t[j] = v[0][j] + bias[j];
+        for (int j = 0; j < 4; ++j)
+          t[j] = v[0][j] + bf16_bits_to_f32((j < 2 ? bias.x : bias.y) >> (16 * (j & 1)) & 0xFFFFu);
         if (a.act == 1) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) t[j] = gelu_erf(t[j]);
