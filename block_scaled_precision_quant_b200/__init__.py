@@ -675,8 +675,8 @@ def gated_grad_quant(dh, gu, act=BQ_GATE_SILU, stochastic=False, seed=0, out=Non
     [2 N, M], sf_t); d (bf16 [M, 2 N]) is written when given."""
     q_row, sf_row, q_t, sf_t = (None,) * 4 if out is None else out
     return (_native or _load_native()).gated_grad_quant(
-        dh, gu, act, BQ_ROUND_STOCHASTIC if stochastic else BQ_ROUND_NEAREST, seed, q_row, sf_row,
-        q_t, sf_t, d, status)
+        dh, gu, act, BQ_ROUND_STOCHASTIC if stochastic else BQ_ROUND_NEAREST, int(seed), q_row,
+        sf_row, q_t, sf_t, d, status)
 
 
 config = _config

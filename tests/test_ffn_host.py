@@ -110,6 +110,23 @@ def test_binding_refusals():
                             torch.zeros((32, 64), dtype=torch.bfloat16))
 
 
+def test_binding_argument_types():
+    i8, f = torch.zeros((4, 32), dtype=torch.int8), torch.zeros(32)
+    for bad in (None, 3, [1.0]):
+        with pytest.raises(TypeError):
+            bq.act_quant_int8(bad)
+        with pytest.raises(TypeError):
+            bq.gemm_int8_int8(i8, bad, i8, f, 4, 4, 32)
+        with pytest.raises(TypeError):
+            bq.gemm_gated(bq.W_INT8, i8, f, bad, f, i8, f, 4, 4, 32)
+        with pytest.raises(TypeError):
+            bq.gated_grad_quant(f, bad)
+    with pytest.raises(TypeError):
+        bq.gemm_int8_int8(i8, f, i8, f, 4.0, 4, 32)
+    with pytest.raises(TypeError):
+        bq.gemm_int8_int8(i8, f, i8, f, 4, 4, 32, alpha="1")
+
+
 def test_plans():
     def p(M, N, K, **kw):
         c = bq.ffn_plan(M, N, K, **kw)

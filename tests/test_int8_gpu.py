@@ -295,6 +295,55 @@ def test_residual_in_place():
         assert torch.equal(got, ref)
 
 
+def test_binding_refuses_what_the_operands_do_not_hold():
+    x = rows(8, 64, 1)
+    q, s = bq.act_quant_int8(x)
+    b, sb = bq.act_quant_int8(rows(16, 64, 2))
+    y = torch.empty((8, 16), dtype=torch.bfloat16, device="cuda")
+    assert bq.gemm_int8_int8(q, s, b, sb, 8, 16, 64, y=y) is y
+    for kw in (dict(y=y[:4]), dict(y=y.float()), dict(y=y.t()), dict(bias=y[0, :8]),
+               dict(bias=torch.zeros(16, device="cuda")), dict(residual=y[:4]),
+               dict(residual=y.t()), dict(residual=y.cpu())):
+        with pytest.raises(ValueError):
+            bq.gemm_int8_int8(q, s, b, sb, 8, 16, 64, **kw)
+    for M, N, K in ((9, 16, 64), (8, 24, 64), (8, 16, 80)):  # more than the operands have
+        with pytest.raises(ValueError):
+            bq.gemm_int8_int8(q, s, b, sb, M, N, K)
+    for args in ((q.float(), s, b, sb), (q, s.double(), b, sb), (q.t(), s, b, sb),
+                 (q, s.cpu(), b, sb)):
+        with pytest.raises(ValueError):
+            bq.gemm_int8_int8(*args, 8, 16, 64)
+    with pytest.raises(ValueError):
+        bq.act_quant_int8(x.float())
+    with pytest.raises(ValueError):
+        bq.act_quant_int8(x.t())
+    for M, N, K in ((-1, 16, 64), (8, -8, 64), (8, 16, 0), (8, 12, 64), (8, 16, 24)):
+        with pytest.raises(bq.BqError) as e:
+            bq.gemm_int8_int8(q, s, b, sb, M, N, K)
+        assert e.value.status == bq.BQ_ERR_SHAPE
+    torch.cuda.synchronize()
+
+
+def test_two_host_threads_at_once():
+    from concurrent.futures import ThreadPoolExecutor
+    x = [rows(41, 512, i) for i in range(2)]
+    b, sb = bq.act_quant_int8(rows(768, 512, 9))
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(200):
+                q, s = bq.act_quant_int8(x[i])
+                y = bq.gemm_int8_int8(q, s, b, sb, 41, 768, 512)
+            torch.cuda.current_stream().synchronize()
+        return y
+    with ThreadPoolExecutor(2) as pool:
+        got = list(pool.map(work, range(2)))
+    for i in range(2):
+        q, s = bq.act_quant_int8(x[i])
+        assert torch.equal(got[i], bq.gemm_int8_int8(q, s, b, sb, 41, 768, 512))
+
+
 def test_empty_calls():
     a, b = Operand("int8", 4, 32, 1), Operand("int8", 8, 32, 2)
     assert bq.gemm_int8_int8(a.q[:0], a.sf[:0], b.q, b.sf, 0, 8, 32).shape == (0, 8)
