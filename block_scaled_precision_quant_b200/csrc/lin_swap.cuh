@@ -30,9 +30,9 @@
 
 namespace bq {
 
-// Warps: 0 weight tile copies, 1 TMEM and MMA issue, 2-5 accumulator copies
-// to shared memory, 6 activation tile copies, 7 weight scale copies, 8
-// activation scale copies, 9 the second weight's tile copies.
+// Warps: 0 weight tile copies, 1 TMEM and MMA issue, 6 activation tile copies, 7
+// weight scale copies, 8 activation scale copies, 9 the second weight's tile copies;
+// 2-9 then take the sums to shared memory.
 constexpr int kSwapThreads = 320;
 constexpr int kSwapWarps = kSwapThreads / 32;
 
@@ -67,6 +67,12 @@ struct SwapSmem {
   static_assert(kBytes <= (OCC == 2 ? 115712 : 232448), "shared memory budget");
   static_assert(OCC * kTmemCols <= 512, "TMEM of co-resident CTAs");
 };
+
+// Cluster barrier for leaving: orders nothing, so it does not wait for the outputs'
+// stores.  Each thread has used what it read of its peers' shared memory by then.
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
 
 // Four consecutive sums of one row and weight, at this shared-memory address in
 // each CTA of the cluster, all slices in rank order.
@@ -152,32 +158,6 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-
-  const int mt = min(BN, a.M - m0);
-  auto sums_to_smem = [&] {
-    // Sums to shared memory: a lane holds one output n, a warp store is 32
-    // consecutive n of one row m.  Every MMA that read the stages is complete.
-    const int quad = warp % 4;
-    const int row = quad * 32 + lane;
-    if (mbar_wait(tfull, 0, a.err, abort_flag, kWaitEpiFull)) {
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-#pragma unroll
-      for (int w = 0; w < L::kWeights; ++w) {
-        uint32_t *dst = reinterpret_cast<uint32_t *>(smem + w * L::kPart) + row;
-#pragma unroll 1
-        for (int c = 0; c < BN / 32 && c * 32 < mt; ++c) {
-          uint32_t v[32];
-          __syncwarp();
-          tmem_ld_32x32b_x32(t_row + w * BN + c * 32, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) dst[(c * 32 + j) * kBlockP] = v[j];
-        }
-      }
-    }
-  };
 
   const bool copier = warp == 0 || warp == 6 || (!I8 && (warp == 7 || warp == 8)) ||
                       (GATED && warp == 9);
@@ -274,16 +254,14 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
       tc_commit(drain);
       if (!mbar_wait_timed(drain, 0, a.err, kWaitDrain)) sleep_ns(200000);
     }
-  } else if (!I8 && warp >= 2 && warp <= 5) {
-    sums_to_smem();
   }
   __syncwarp();
   // The scales, bias and residual may come from the preceding kernel, which
   // may also still read or write the outputs.
   griddep_wait();
   // What the outputs need besides the sums, fetched while those are formed (int8 41 x
-  // 1536 x 6144: 7.0 us with the scales fetched behind the exchange, 6.6 so; MX has
-  // none, and 0.15 us more in this order).
+  // 1536 x 6144: 7.0 us with the scales fetched behind the exchange, 6.6 so).
+  const int mt = min(BN, a.M - m0);
   const int n = n0 + 4 * lane;
   const bool nok = n < a.N;
   float sw[2][4];
@@ -300,7 +278,27 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
   if (!GATED && a.bias && nok) bias = __ldg(reinterpret_cast<const uint2 *>(a.bias + n));
   const int first = rank * kSwapWarps + warp;  // this warp's first row
   float sa = I8 && first < mt ? __ldg(a.sa + b * a.sa_bstride + m0 + first) : 1.0f;
-  if (I8 && warp >= 2 && warp <= 5) sums_to_smem();
+  if (warp >= 2 && mbar_wait(tfull, 0, a.err, abort_flag, kWaitEpiFull)) {
+    // Sums to shared memory: a lane holds one output n, a warp store is 32
+    // consecutive n of one row m.  Every MMA that read the stages is complete.  Two
+    // warps to a quadrant of the TMEM lanes, 32 rows (of one weight) a turn.
+    const int quad = warp % 4;
+    __syncwarp();
+    tc_fence_after();
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(smem) + quad * 32 + lane;
+    const int chunks = (mt + 31) / 32;
+#pragma unroll 1
+    for (int i = (warp - 2) / 4; i < L::kWeights * chunks; i += 2) {
+      const int w = GATED && i >= chunks ? 1 : 0, c = i - w * chunks;
+      uint32_t v[32];
+      __syncwarp();
+      tmem_ld_32x32b_x32(t_row + w * BN + c * 32, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) dst[w * (L::kPart / 4) + (c * 32 + j) * kBlockP] = v[j];
+    }
+  }
   __syncwarp();
   tc_fence_before();
   if (S > 1)
@@ -401,7 +399,7 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
   }
   // No CTA leaves while a peer still reads its sums.
   if (S > 1)
-    cluster_sync_all();
+    cluster_leave();
   else
     __syncthreads();
   if (warp == 1) {
