@@ -227,7 +227,10 @@ int make_plan(Kind kind, bool gated, int64_t M, int64_t N, int64_t K, int64_t ba
   // One CTA to an SM has twice the stages: it streams faster where there are no
   // more tiles than SMs (int8 512 x 4096 x 4096 in 128-row tiles: 14.0 us, 16.1
   // with two); two take the tiles beyond that (1024 x 4096 x 4096: 28.1 and 21.5).
-  p->occ = p->splits == 1 && p->tiles <= num_sms ? 1 : 2;
+  // In clusters of two as well (gated MXFP8 41 x 8192 x 2048: 10.9 and 13.0, int8 41 x
+  // 8192 x 4096: 9.9 and 10.4), but for packed weights, half the bytes (gated MXFP4 16
+  // x 9216 x 2048: 8.6 and 8.2); longer clusters find too few places.
+  p->occ = p->splits <= (kind == kMxfp4 ? 1 : 2) && p->tiles * p->splits <= num_sms ? 1 : 2;
   return p->tiles * p->splits > 0x7FFFFFFF ? BQ_ERR_SHAPE : BQ_OK;
 }
 
