@@ -158,29 +158,35 @@ int check_config(const bq_gemm_config* cfg) {
   return BQ_OK;
 }
 
-// Estimated microseconds of the two schedules, fitted to sweeps over 1 to 2750
-// rows, 376 to 16384 outputs and K of 304 to 9008 (most within 15 %).
-//   swap: launch, first copies and outputs 3.8 us, longer by the tile's rows.  A CTA
-//         fills its shared memory at about 105 KB/us, all of them at 12 GB/ms from
-//         L2.  A split adds the exchange (int8 41 x 4608 x 1536: 6.4 us unsplit, 6.1
-//         in 4 slices; 41 x 1536 x 6144: 14.5 and 6.7 in 8; gated 41 x 6144 x 1536:
-//         10.4 and 8.6 in 2, 9.3 in 4), more CTAs than SMs their start (int8 795 x
-//         4176 x 304: 11.0 in 64-row tiles, 8.5 in 128-row ones, 7.7 in pairs).
-//   pair: 6.3 us (gated 7.5) and 0.29 us a K block of 256 x 256 (int8 256 x 4096 x
-//         4096: 15.6 us, 12.0 as 64-row tiles; 1024 x 4096 x 4096: 17.8, 28 as
-//         128-row tiles; 512 x 1024 x 1024: 8.4, 5.6 as 64-row tiles).
-double swap_us(int bn, int64_t tiles, int splits, int kt, bool gated, int num_sms) {
-  const double ctas = static_cast<double>(tiles * splits);
-  const double kb = static_cast<double>(kt) / splits * ((gated ? 32 : 16) + bn / 8.0);  // a CTA's
+// Estimated microseconds of the two schedules, fitted to 260 random problems of 1 to
+// 1500 rows, 256 to 16384 outputs and K of 256 to 8192, each measured in every
+// schedule (a mean of 10 % off; the schedules picked take 1.3 % more than the best).
+//   swap: launch, first copies and outputs 3 us (MX 4.1), longer by the tile's rows.  A
+//         CTA fills its shared memory at 105 KB/us (packed weights at their unpacked
+//         size), all of them at 8.3 GB/ms from L2.  A split adds the exchange (int8 41
+//         x 4608 x 1536: 6.4 us unsplit, 5.4 in 4 slices; 41 x 1536 x 6144: 14.5 and 5.6
+//         in 8; gated MXFP4 41 x 6144 x 1536: 10.4 and 8.5 in 2 or 4), more CTAs than SMs
+//         their start.
+//   pair: 5.1 us and 0.26 us (MX 0.33) a K block of 256 x 256 (int8 256 x 4096 x 4096:
+//         15.6 us, 12.0 as 64-row tiles; 1024 x 4096 x 4096: 17.8, 28 as 128-row tiles).
+double swap_us(Kind kind, bool gated, int bn, int64_t M, int64_t tiles, int splits, int kt,
+               int num_sms) {
+  const double ctas = static_cast<double>(tiles * splits), weights = gated ? 2 : 1;
+  const double rows = static_cast<double>(std::min<int64_t>(M, bn)) / 128;
+  const double blocks = static_cast<double>(kt) / splits;  // a CTA's
+  const double kb = blocks * (16 * weights + bn / 8.0);
+  const double l2 = blocks * ((kind == kMxfp4 ? 8 : 16) * weights + bn / 8.0);
   const double starts =
-      ctas <= num_sms ? 0.0 : 1.5 + 3.5 * static_cast<double>((tiles * splits - 1) / (2 * num_sms));
-  return 3.8 + bn / 128.0 * 0.8 * (gated ? 2 : 1) + starts + std::max(kb / 105, ctas * kb / 12e3) +
-         (splits > 1 ? bn / 64.0 * 1.6 : 0.0);
+      ctas <= num_sms ? 0.0 : 0.4 + 3.5 * static_cast<double>((tiles * splits - 1) / (2 * num_sms));
+  return (kind == kInt8 ? 3.0 : 4.1) + 2.2 * rows * weights + starts +
+         std::max(kb / 105, ctas * l2 / 8.3e3) +
+         (splits > 1 ? 0.26 + 0.26 * rows * weights / splits + 0.1 * splits : 0.0);
 }
 
-double pair_us(int64_t tiles, int kt, bool gated, int num_sms) {
+double pair_us(Kind kind, bool gated, int64_t tiles, int kt, int num_sms) {
   const int64_t waves = ceil_div(tiles, num_sms / 2);
-  return (gated ? 7.5 : 6.3) + static_cast<double>(waves) * (kt * 0.29 + (gated ? 1.0 : 0.5));
+  return 5.1 + static_cast<double>(waves) *
+                   (kt * (kind == kInt8 ? 0.264 : 0.33) + (gated ? 1.4 : 0.3));
 }
 
 int make_plan(Kind kind, bool gated, int64_t M, int64_t N, int64_t K, int64_t batch,
@@ -199,13 +205,17 @@ int make_plan(Kind kind, bool gated, int64_t M, int64_t N, int64_t K, int64_t ba
   double best = 1e30;
   for (int bn = 32; bn <= 128 && !pair_asked; bn *= 2) {
     if (c.block_n ? bn != c.block_n
-                  : (bn < 128 && M > bn && (bn == 32 || kind != kInt8)) || (bn > 32 && M <= bn / 2))
+                  : (bn < 128 && M > (kind == kInt8 ? bn == 32 ? 256 : M : bn)) ||
+                        (bn > 32 && M <= bn / 2))
       continue;
     const int64_t tiles_q = ceil_div(M, bn), tiles = tiles_p * tiles_q * batch;
     for (int s = c.split_k ? c.split_k : 1; s <= (c.split_k ? c.split_k : kMaxSplit); s *= 2) {
-      // a split's clusters find a place at once up to about nine tenths of the SMs
-      if (!c.split_k && s > 1 && (p->kt / s < 2 || tiles * s * 10 > num_sms * 18)) break;
-      const double us = swap_us(bn, tiles, s, p->kt, gated, num_sms);
+      // a split's clusters find a place at once up to about nine tenths of the places,
+      // two an SM (gated 128-row tiles: eight tenths of one)
+      if (!c.split_k && s > 1 &&
+          (p->kt / s < 2 || tiles * s * 10 > num_sms * (gated && bn == 128 ? 8 : 18)))
+        break;
+      const double us = swap_us(kind, gated, bn, M, tiles, s, p->kt, num_sms);
       if (us >= best) continue;
       best = us;
       p->bn = bn;
@@ -216,7 +226,7 @@ int make_plan(Kind kind, bool gated, int64_t M, int64_t N, int64_t K, int64_t ba
   }
   p->pair = pair_asked ||
             (!swap_asked && M > 64 &&
-             pair_us(pair_p * pair_q * batch, p->kt, gated, num_sms) < best);
+             pair_us(kind, gated, pair_p * pair_q * batch, p->kt, num_sms) < best);
   if (p->pair) {
     p->bn = 256;
     p->splits = 1;
