@@ -593,7 +593,7 @@ _native = None
 
 def _load_native():
     """The compiled calls of these operators (csrc/torch_calls.cpp): argument checks,
-    output tensors and the library call, in a third of the time that they take
+    output tensors and the library call, in less than half the time that they take
     through ctypes, where small calls spend most of it."""
     global _native
     if _native is None:

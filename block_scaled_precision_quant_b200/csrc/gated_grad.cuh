@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(256, 2) gated_grad_sr_kernel(
 //   3. two columns x 32 rows a thread, whole groups: the transposed codes, which
 //      turn around through the tiles' memory and leave as 128-byte lines.
 // Floor: 6 bytes read and 4.1 written for each element of F.  Bound by the
-// instructions it issues, 46 an element (63 in a version that kept one ownership
-// and met by shuffles): 4096 x 6144 56 us, 4.5 TB/s (GELU 65; bq_grad_quant_dual
-// of a ready [4096, 12288] gradient 88).
+// instructions it issues (46 an element before pairs of values took one, 63 in a
+// version that kept one ownership and met by shuffles): 4096 x 6144 53 us, 4.8 TB/s
+// (GELU 59 to 66; bq_grad_quant_dual of a ready [4096, 12288] gradient 88).
 struct GradSmem {
   static constexpr int kTile = 128 * 256;         // [128 rows][128 bf16]: g, u, dH
   static constexpr int kOffSfr = 3 * kTile;       // [2][128 rows][4 groups]

@@ -22,8 +22,8 @@
 // What bounds it: the weights are read once per BN rows, so HBM for large
 // weights, and for small ones the chain launch - first copies - MMAs - exchange.
 // Measured: gated FP8 16 x 16384 x 8192 (277 MB) 46 us, 6.0 TB/s, 94 % of the copy
-// rate; gated MXFP4 41 x 6144 x 1536 8.4 us (unsplit 10.3, 3 slices 9.2); int8 with
-// a bias 1 x 4608 x 1536 4.8 us.
+// rate; gated MXFP4 41 x 6144 x 1536 8.5 us (unsplit 10.4); int8 with a bias
+// 1 x 4608 x 1536 4.3 us (unsplit 5.3).
 #pragma once
 
 #include "ffn_args.cuh"
