@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
     const int64_t groups = a.N >> 5, katoms = (groups + 3) >> 2;
     // One row a warp and round, in code that is short: it runs once, from a cold
     // instruction cache (four rows a round, fetched together, took 0.5 to 2 us
-    // longer on 41 x 1536 x 6144 split eight ways and gained nothing elsewhere).
+    // longer on 41 x 1536 x 6144 split eight ways and gained nothing elsewhere; four
+    // slices' loads under way at once 0.1 to 0.4 us longer with 41 rows).
 #pragma unroll 1
     for (int r = first; r < mt; r += S * kSwapWarps) {
       const int m = m0 + r;
