@@ -300,12 +300,13 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
     const uint32_t lead_tempty = mapa_shared(smem_u32(tempty), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    uint32_t rphase = 0;  // residual barriers' parity: the same for all
+    uint32_t rphase = 0;  // bit i: parity of staging tile i's residual barrier
     griddep_wait();  // scales, bias and residual may come from the kernel before
     for (int unit = pair; unit < total_units; unit += num_pairs) {
       const UnitPos u = unit_pos(a, unit);
       const int m0 = (2 * u.tp + static_cast<int>(rank)) * 128, m = m0 + row;
       const int n0 = u.tq * kTileN;
+      const int nch = min(kTileN / 32, (a.N - n0 + 31) / 32);
       // what the outputs need besides the sums, fetched while the sums are formed
       const float sa = m < a.M ? __ldg(a.sa + u.b * a.sa_bstride + m) : 0.0f;
       float sw[2], bias[2];
@@ -318,8 +319,11 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
       }
       if (RES && out.tid == 0) {
         bulk_wait_group_read<0>();  // earlier stores have read the staging tiles
+        // Only chunks that exist: the group meets (group_sync) behind each wait for a
+        // chunk, so no thread arms a barrier again that another has yet to wait on.
 #pragma unroll
         for (int i = 0; i < L::kSlots; ++i) {
+          if (group + kPairGroups * i >= nch) break;
           uint64_t *bar = &rbar[group * L::kSlots + i];
           mbar_arrive_expect_tx(bar, static_cast<uint32_t>(kYChunkBytes));
           tma_load_3d(out.slot + i * kYChunkBytes, &tm_g, bar,
@@ -331,7 +335,6 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
       __syncwarp();
       tc_fence_after();
       const uint32_t t_row = tmem_base + acc * 256 + (static_cast<uint32_t>(quad * 32) << 16);
-      const int nch = min(kTileN / 32, (a.N - n0 + 31) / 32);
       if constexpr (GATED) {
         // This group's 32 outputs: all sums into registers, then their TMEM goes
         // back to the MMAs.
@@ -354,13 +357,16 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int c = group + kPairGroups * i;
-          if (RES && !mbar_wait(&rbar[group * L::kSlots + i * (L::kSlots - 1)], rphase, a.err,
-                                abort_flag, kWaitEpiFull)) {
-            ok = false;
-            break;
+          if (c >= nch) break;  // uniform
+          if constexpr (RES) {
+            if (!mbar_wait(&rbar[group * L::kSlots + i], rphase >> i & 1u, a.err, abort_flag,
+                           kWaitEpiFull)) {
+              ok = false;
+              break;
+            }
+            rphase ^= 1u << i;
           }
           __syncwarp();
-          if (c >= nch) continue;  // uniform
           const int q0 = n0 + c * 32;
           uint32_t v[32];
           tmem_ld_32x32b_x32(t_row + c * 32, v);
@@ -404,7 +410,6 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
           }
         }
         if (!ok) break;
-        rphase ^= 1;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(lead_tempty + acc * 8);

@@ -171,6 +171,29 @@ def test_pair_tiles_in_several_waves(K, bias, res, act):
     product(2900, 3336, K, K, bias, res, act, 0.5, bq.config(swap_ab=0))
 
 
+# the last column of tiles holds 1 to 8 of its 8 chunks of 32 outputs, so that the epilogue's
+# groups have two, one or none of their own; short sums, many tiles a pair: the epilogue is
+# what the tiles wait for
+@pytest.mark.parametrize("tail", [8, 40, 96, 104, 136, 160, 224, 248, 256])
+@pytest.mark.parametrize("full", [0, 2])
+def test_pair_tiles_residual_in_narrow_last_columns(tail, full):
+    M, N, K = 256 * 150 // (full + 1) - 100, 256 * full + tail, 16
+    a, b = Operand("int8", M, K, tail), Operand("int8", N, K, tail + 1)
+    res = (torch.randn((M, N), device="cuda") * 3).to(torch.bfloat16)
+    want = bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, M, N, K, residual=res,
+                             config=bq.config(swap_ab=1, block_n=128))
+    got = []
+    for _ in range(20):
+        y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+        got.append(bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, M, N, K, residual=res, y=y,
+                                     config=bq.config(swap_ab=0)))
+    bq.device_status()  # no wait gave up
+    p = ffn_ref.product(a, b)
+    r = res.double()
+    close(want, p + r, int8_tol(p, torch.zeros_like(p), p, r, p + r, 0))
+    assert all(torch.equal(want, y) for y in got)
+
+
 def test_pair_tiles_equal_swap_tiles():
     a, b = Operand("int8", 300, 1552, 5), Operand("int8", 776, 1552, 6)
     ys = [bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, 300, 776, 1552, config=c)
