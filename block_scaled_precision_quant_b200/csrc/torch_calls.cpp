@@ -120,9 +120,22 @@ void need_rows(const Tensor &t, int64_t rows, int64_t cols, const char *what) {
                   std::to_string(cols) + "] tensor with unit column stride");
 }
 
-// Row stride of a 2-D tensor (one row has none of its own).
+// Row stride of a tensor's last two dimensions (one row has none of its own).
 int64_t row_stride(const Tensor &t) {
-  return t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1));
+  return t.size(-2) > 1 ? t.stride(-2) : std::max(t.stride(-2), t.size(-1));
+}
+
+// bf16 rows of unit column stride for a batch whose last problem begins
+// `last` elements behind the first: the strides are the
+// caller's, so what counts is what the storage holds.
+void need_batch_rows(const Tensor &t, int64_t rows, int64_t cols, Wide last, const char *what) {
+  if (t.scalar_type() != at::kBFloat16 || t.dim() < 2 || t.size(-2) < rows || t.size(-1) < cols ||
+      (cols > 1 && t.stride(-1) != 1))
+    throw Refusal(std::string(what) + " must be bf16 [.., " + std::to_string(rows) + ", " +
+                  std::to_string(cols) + "] with unit column stride");
+  const Wide held = Wide(t.storage().nbytes() / t.element_size()) - t.storage_offset();
+  if (rows > 0 && cols > 0 && last + Wide(rows - 1) * row_stride(t) + cols > held)
+    throw Refusal(std::string(what) + " does not reach the last problem's last row");
 }
 
 void *ptr(const Tensor *t) { return t ? t->data_ptr() : nullptr; }
@@ -222,14 +235,6 @@ PyObject *gemm_int8_int8(PyObject *const *a) {
   bq_epilogue epi = {};
   epi.alpha = static_cast<float>(number(a[10]));
   epi.act = static_cast<int>(integer(a[11]));
-  Here here;
-  here.on(aq);
-  here.on(as);
-  here.on(b);
-  here.on(bs);
-  here.on(y_in);
-  here.on(bias);
-  here.on(res);
   bq_batch batch = {1, 0, 0, 0, 0, 0, 0};
   const bool batched = a[12] != Py_None;
   if (batched) {
@@ -254,16 +259,15 @@ PyObject *gemm_int8_int8(PyObject *const *a) {
     epi.bias = ptr(bias);
   }
   if (res) {
-    if (!batched) {
+    if (batched)
+      need_batch_rows(*res, M, N, more * (batch.stride_res / 2), "residual");
+    else
       need_rows(*res, M, N, "residual");
-      epi.ld_residual = row_stride(*res);
-    } else {
-      if (res->scalar_type() != at::kBFloat16 || res->dim() < 2 || res->stride(-1) != 1)
-        throw Refusal("residual must be bf16 with unit column stride");
-      epi.ld_residual = res->stride(-2);
-    }
+    epi.ld_residual = row_stride(*res);
     epi.residual = ptr(res);
   }
+  Here here;
+  for (const Tensor *t : {&aq, &as, &b, &bs, y_in, bias, res}) here.on(t);
   Tensor y = output(y_in, at::kBFloat16, Wide(M) * N + more * (batch.stride_y / 2), "y", [&] {
     return M < 0 || N < 0 || batch.count < 0 ? Tensor()  // refused below
            : batched                         ? here.empty({batch.count, M, N}, at::kBFloat16)

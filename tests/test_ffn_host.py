@@ -127,6 +127,47 @@ def test_binding_argument_types():
         bq.gemm_int8_int8(i8, f, i8, f, 4, 4, 32, alpha="1")
 
 
+def batched_product(M, N, K, count, residual, stride_res):
+    z = torch.zeros
+    return bq.gemm_int8_int8(
+        z((count, M, K), dtype=torch.int8), z(count * M), z((count, N, K), dtype=torch.int8),
+        z(count * N), M, N, K, residual=residual,
+        batch=dict(count=count, stride_a=M * K, stride_a_sf=4 * M, stride_b=N * K,
+                   stride_b_sf=4 * N, stride_y=2 * M * N, stride_res=stride_res))
+
+
+def test_binding_refuses_a_batched_residual_that_ends_early():
+    """The kernels go by the strides alone: the residual's storage has to reach the last
+    problem's last row.  (What passes this check is refused for being on the CPU.)"""
+    M, N, K, count = 5, 16, 32, 3
+    bf = dict(dtype=torch.bfloat16)
+    step = 2 * M * N
+    whole = torch.zeros((count, M, N), **bf)
+    wide = torch.zeros((count, M, 24), **bf)
+    fits = [(whole, step), (whole.view(count * M, N), step), (whole[0], 0), (whole[1], step // 2),
+            (wide, 2 * M * 24), (wide[:, :, :N], 2 * M * 24), (wide[:, :, 8:], 2 * M * 24),
+            (torch.zeros((M, 1, N), **bf).transpose(0, 1), 0)]
+    for res, stride in fits:
+        with pytest.raises(ValueError, match="CUDA tensors only"):
+            batched_product(M, N, K, count, res, stride)
+    short = [(whole[:2].clone(), step, "last row"), (whole, step + 16, "last row"),
+             (whole[1], step, "last row"), (whole[0].clone(), step, "last row"),
+             (wide[1:, :, 8:], 2 * M * 24, "last row"),
+             (torch.zeros((count, M - 1, N), **bf), step, "unit column"),
+             (torch.zeros((count, M, N - 8), **bf), step, "unit column"),
+             (torch.zeros((M, count, N), **bf), step, "unit column"),
+             (torch.zeros((count, N, M), **bf).transpose(1, 2), step, "unit column"),
+             (torch.zeros((M * N,), **bf), 0, "unit column"),
+             (whole.float(), step, "unit column")]
+    for res, stride, why in short:
+        with pytest.raises(ValueError, match=why):
+            batched_product(M, N, K, count, res, stride)
+    # one row has no stride of its own
+    one = torch.zeros((count, 2, N), **bf)[:, :1]
+    with pytest.raises(ValueError, match="CUDA tensors only"):
+        batched_product(1, N, K, count, one, 4 * N)
+
+
 def test_plans():
     def p(M, N, K, **kw):
         c = bq.ffn_plan(M, N, K, **kw)
