@@ -444,6 +444,7 @@ extern "C" {
 int bq_act_quant_int8(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, void* q_s8,
                       float* scale, int* d_status, bq_stream_t stream) {
   if (M < 0 || M > 0x7FFFFFFF || K <= 0 || K % 16 != 0 || ldx < K) return BQ_ERR_SHAPE;
+  if (!aligned(d_status, 4)) return BQ_ERR_ALIGN;
   if (M > 0) {
     if (!x_bf16 || !q_s8 || !scale) return BQ_ERR_NULL;
     if (!aligned(x_bf16, 16) || ldx % 8 != 0 || !aligned(q_s8, 16) || !aligned(scale, 4))
@@ -562,6 +563,7 @@ int bq_gated_grad_quant(const void* dh_bf16, int64_t ld_dh, const void* gu_bf16,
     return BQ_ERR_SHAPE;
   const int64_t groups = ceil_div(M, 128) * 4, tiles = ceil_div(N, 64);
   if (groups > 0x7FFFFFFF || ceil_div(tiles, 2) > 65535) return BQ_ERR_SHAPE;
+  if (!aligned(d_status, 4)) return BQ_ERR_ALIGN;
   if (M > 0) {
     if (!dh_bf16 || !gu_bf16 || !q_row || !sf_row || !q_t || !sf_t) return BQ_ERR_NULL;
     if (!aligned(dh_bf16, 16) || !aligned(gu_bf16, 16) || ld_dh % 8 != 0 || ld_gu % 8 != 0 ||

@@ -112,6 +112,12 @@ void need(const Tensor &t, ScalarType type, Wide count, const char *what) {
                   " elements");
 }
 
+// The word that a quantizer reports a NaN or Inf in.
+void need_status(const Tensor *t) {
+  if (t && (t->scalar_type() != at::kInt || t->numel() < 1))
+    throw Refusal("status must be a torch.int32 tensor of at least 1 element");
+}
+
 // bf16 [rows, cols] with unit column stride (the row stride may exceed cols).
 void need_rows(const Tensor &t, int64_t rows, int64_t cols, const char *what) {
   if (t.scalar_type() != at::kBFloat16 || t.dim() != 2 || t.size(0) != rows ||
@@ -205,6 +211,7 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *act_quant_int8(PyObject *const *a) {
   const Tensor &x = need_tensor(a[0]);
   const Tensor *q_in = tensor(a[1]), *scale_in = tensor(a[2]), *status = tensor(a[3]);
+  need_status(status);
   Here here;
   here.on(x);
   here.on(q_in);
@@ -350,6 +357,7 @@ PyObject *gated_grad_quant(PyObject *const *a) {
   if (PyErr_Occurred()) throw Raised{};
   const Tensor *out[4] = {tensor(a[5]), tensor(a[6]), tensor(a[7]), tensor(a[8])};
   const Tensor *d = tensor(a[9]), *status = tensor(a[10]);
+  need_status(status);
   Here here;
   here.on(dh);
   here.on(gu);

@@ -509,7 +509,7 @@ size_t bq_noalloc_scratch_bytes(void);
  *           16-byte aligned); K > 0 and K % 16 == 0
  *   q_s8    out [M, K] signed 8-bit codes (-127 .. 127), row stride K, 16-byte aligned
  *   scale   out [M] fp32, 4-byte aligned
- *   d_status as bq_act_quant (a row with a NaN or Inf is unspecified).
+ *   d_status as bq_act_quant, 4-byte aligned (a row with a NaN or Inf is unspecified).
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_ARCH, BQ_ERR_CUDA. */
 int bq_act_quant_int8(const void *x_bf16, int64_t M, int64_t K, int64_t ldx, void *q_s8,
                       float *scale, int *d_status, bq_stream_t stream);
@@ -595,7 +595,7 @@ int bq_ffn_plan(int weight_kind, int gated, int64_t M, int64_t N, int64_t K, int
  *   keeps it (row stride ld_gu >= 2 N); M % 32 == 0, N % 32 == 0, strides % 8 == 0,
  *   bases 16-byte aligned
  *   d_bf16  optional out [M, 2 N] bf16, 16-byte aligned: d itself
- *   d_status as bq_act_quant, of d.
+ *   d_status as bq_act_quant, of d, 4-byte aligned
  * Errors: as bq_grad_quant_dual, BQ_ERR_INVALID for a bad act. */
 int bq_gated_grad_quant(const void *dh_bf16, int64_t ld_dh, const void *gu_bf16, int64_t ld_gu,
                         int64_t M, int64_t N, int act, int rounding, uint64_t seed, void *q_row,

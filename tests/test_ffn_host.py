@@ -168,6 +168,26 @@ def test_binding_refuses_a_batched_residual_that_ends_early():
         batched_product(1, N, K, count, one, 4 * N)
 
 
+def test_status_is_an_int32_word(L):
+    x = torch.zeros((32, 32), dtype=torch.bfloat16)
+    gu = torch.zeros((32, 64), dtype=torch.bfloat16)
+    for bad in (torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.int64),
+                torch.zeros(0, dtype=torch.int32), torch.zeros(4)):
+        with pytest.raises(ValueError, match="status must be a torch.int32"):
+            bq.act_quant_int8(x, status=bad)
+        with pytest.raises(ValueError, match="status must be a torch.int32"):
+            bq.gated_grad_quant(x, gu, status=bad)
+    for good in (torch.zeros((), dtype=torch.int32), torch.zeros(4, dtype=torch.int32)[1::2]):
+        with pytest.raises(ValueError, match="CUDA tensors only"):
+            bq.act_quant_int8(x, status=good)
+        with pytest.raises(ValueError, match="CUDA tensors only"):
+            bq.gated_grad_quant(x, gu, status=good)
+    assert L.bq_act_quant_int8(P, 4, 32, 32, P, P, P + 2, None) == bq.BQ_ERR_ALIGN
+    for rounding in (0, 1):
+        assert L.bq_gated_grad_quant(P, 64, P, 128, 32, 64, 0, rounding, 0, P, P, P, P, None,
+                                     P + 2, None) == bq.BQ_ERR_ALIGN
+
+
 def test_plans():
     def p(M, N, K, **kw):
         c = bq.ffn_plan(M, N, K, **kw)
