@@ -567,7 +567,8 @@ int bq_gated_grad_quant(const void* dh_bf16, int64_t ld_dh, const void* gu_bf16,
   if (M > 0) {
     if (!dh_bf16 || !gu_bf16 || !q_row || !sf_row || !q_t || !sf_t) return BQ_ERR_NULL;
     if (!aligned(dh_bf16, 16) || !aligned(gu_bf16, 16) || ld_dh % 8 != 0 || ld_gu % 8 != 0 ||
-        !aligned(q_row, 16) || !aligned(q_t, 16) || !aligned(d_bf16, 16))
+        !aligned(q_row, 16) || !aligned(q_t, 16) || !aligned(sf_row, 4) || !aligned(sf_t, 4) ||
+        !aligned(d_bf16, 16))
       return BQ_ERR_ALIGN;
   }
   Device dev;

@@ -593,7 +593,7 @@ int bq_ffn_plan(int weight_kind, int gated, int64_t M, int64_t N, int64_t K, int
  *   dW = bq_gemm_e5m2_mxfp8(q_t, bq_quant_transposed(X), 2 N, K, M).
  *   dh_bf16 [M, N] (row stride ld_dh >= N), gu_bf16 [M, 2 N] as bq_gemm_gated
  *   keeps it (row stride ld_gu >= 2 N); M % 32 == 0, N % 32 == 0, strides % 8 == 0,
- *   bases 16-byte aligned
+ *   bases 16-byte aligned; sf_row and sf_t 4-byte aligned
  *   d_bf16  optional out [M, 2 N] bf16, 16-byte aligned: d itself
  *   d_status as bq_act_quant, of d, 4-byte aligned
  * Errors: as bq_grad_quant_dual, BQ_ERR_INVALID for a bad act. */

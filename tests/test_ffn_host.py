@@ -188,6 +188,15 @@ def test_status_is_an_int32_word(L):
                                      P + 2, None) == bq.BQ_ERR_ALIGN
 
 
+@pytest.mark.parametrize("rounding", [0, 1])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_grad_scale_buffers_are_aligned(L, rounding, off):
+    """The scales leave as words."""
+    for sf, st in ((P + off, P), (P, P + off)):
+        assert L.bq_gated_grad_quant(P, 64, P, 128, 32, 64, 0, rounding, 0, P, sf, P, st, None,
+                                     None, None) == bq.BQ_ERR_ALIGN
+
+
 def test_plans():
     def p(M, N, K, **kw):
         c = bq.ffn_plan(M, N, K, **kw)
