@@ -499,8 +499,9 @@ int bq_gemm_int8_int8_epilogue(const void* a_s8, const float* a_scale, const voi
   }
   if (c.batch.count > 1) {
     const bq_batch& b = c.batch;
+    // outputs of two problems do not share memory: a problem's are 2 M N bytes
     if (b.stride_a < 0 || b.stride_a_sf < 0 || b.stride_b < 0 || b.stride_b_sf < 0 ||
-        b.stride_y <= 0 || b.stride_res < 0)
+        b.stride_y <= 0 || b.stride_y / 2 < M * N || b.stride_res < 0)
       return BQ_ERR_SHAPE;
     if (b.stride_a % 16 || b.stride_b % 16 || b.stride_a_sf % 4 || b.stride_b_sf % 16 ||
         b.stride_y % 16 || b.stride_res % 16)

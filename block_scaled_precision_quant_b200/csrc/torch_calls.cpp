@@ -273,6 +273,8 @@ PyObject *gemm_int8_int8(PyObject *const *a) {
     epi.ld_residual = row_stride(*res);
     epi.residual = ptr(res);
   }
+  if (!y_in && more > 0 && Wide(batch.stride_y) > Wide(M) * N * 2)
+    throw Refusal("a batch with gaps between its outputs (stride_y) needs y");
   Here here;
   for (const Tensor *t : {&aq, &as, &b, &bs, y_in, bias, res}) here.on(t);
   Tensor y = output(y_in, at::kBFloat16, Wide(M) * N + more * (batch.stride_y / 2), "y", [&] {

@@ -524,7 +524,8 @@ int bq_act_quant_int8(const void *x_bf16, int64_t M, int64_t K, int64_t ldx, voi
  * The _epilogue form: y = bf16(act(alpha a_scale b_scale sum + bias) + residual)
  * with bq_epilogue's options except the quantized output (BQ_ERR_INVALID), and
  * bq_batch (its scale strides step the fp32 scales: bytes, multiples of 4 for
- * a_scale, of 16 for b_scale).  It needs no workspace.  Stream order as the
+ * a_scale, of 16 for b_scale; stride_y is at least 2 M N, so that outputs do not
+ * overlap, else BQ_ERR_SHAPE).  It needs no workspace.  Stream order as the
  * GEMMs above: b may be read early (a_scale, b_scale, bias and residual are not).
  * M, N <= 0x7FFFFE00 (here and in bq_gemm_gated).
  * Schedules (bq_gemm_config): swap_ab 1: block_n 32, 64 or 128 activation rows

@@ -197,6 +197,31 @@ def test_grad_scale_buffers_are_aligned(L, rounding, off):
                                      None, None) == bq.BQ_ERR_ALIGN
 
 
+def test_batched_outputs_keep_apart(L):
+    """Problems' outputs (2 M N bytes each) may have gaps between them, in a y that the
+    caller brings, but not overlap."""
+    B = bq.Batch
+    for stride in (16, 48):
+        assert product(L, batch=B(2, 128, 16, 0, 0, stride, 0)) == bq.BQ_ERR_SHAPE
+    # (as far as the alignment that is checked next)
+    assert product(L, batch=B(2, 128, 16, 0, 0, 72, 0)) == bq.BQ_ERR_ALIGN
+    assert product(L, M=0x7FFFFE00, N=0x7FFFFE00, batch=B(2, 0, 0, 0, 0, 1 << 61, 0)) \
+        == bq.BQ_ERR_SHAPE
+    M, N, K, count = 4, 8, 32, 3
+    i8, f = torch.zeros(count * M * K + N * K, dtype=torch.int8), torch.zeros(64)
+
+    def call(stride_y, y=None):
+        bq.gemm_int8_int8(i8, f, i8, f, M, N, K, y=y, batch=dict(
+            count=count, stride_a=M * K, stride_a_sf=4 * M, stride_y=stride_y))
+    dense, gaps = 2 * M * N, 2 * M * N + 64
+    with pytest.raises(ValueError, match="needs y"):
+        call(gaps)
+    held = torch.zeros(2 * (gaps // 2) + M * N, dtype=torch.bfloat16)
+    for stride, y in ((dense, None), (gaps, held)):
+        with pytest.raises(ValueError, match="CUDA tensors only"):
+            call(stride, y)
+
+
 def test_plans():
     def p(M, N, K, **kw):
         c = bq.ffn_plan(M, N, K, **kw)

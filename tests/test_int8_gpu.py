@@ -248,6 +248,21 @@ def test_batch_with_broadcast_operands(M):
             close(y[i], p + r, int8_tol(p, z, p, r, p + r, 0), f"{shared} {i}")
 
 
+@pytest.mark.parametrize("M", [20, 300])
+def test_batch_with_gaps_between_the_outputs(M):
+    count, N, K = 3, 136, 80
+    a = [Operand("int8", M, K, 30 + i) for i in range(count)]
+    b = Operand("int8", N, K, 40)
+    aq, asf = torch.stack([t.q for t in a]), torch.stack([t.sf for t in a])
+    y = torch.full((count, M + 2, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = bq.gemm_int8_int8(aq, asf, b.q, b.sf, M, N, K, y=y, batch=dict(
+        count=count, stride_a=M * K, stride_a_sf=4 * M, stride_y=2 * (M + 2) * N))
+    bq.device_status()
+    assert out is y and bool((y[:, M:] == 9).all())
+    for i in range(count):
+        assert torch.equal(y[i, :M], bq.gemm_int8_int8(a[i].q, a[i].sf, b.q, b.sf, M, N, K))
+
+
 def test_rows_behind_the_last_stay_as_they_were():
     M, N, K = 37, 136, 160
     a, b = Operand("int8", M, K, 1), Operand("int8", N, K, 2)
