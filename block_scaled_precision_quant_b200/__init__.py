@@ -471,9 +471,12 @@ def gemm(weight_kind, a_q, a_sf, b, b_sf, M, N, K, y=None, bias=None, residual=N
         return gemm_int8_int8(a_q, a_sf, b, b_sf, M, N, K, y=y, bias=bias, residual=residual,
                               alpha=alpha, act=act, batch=batch, config=config)
     torch = _torch()
-    _need_cuda(a_q, a_sf, b, b_sf, bias, residual)
     count = 1 if batch is None else int(batch["count"])
     shape = (M, N) if batch is None else (count, M, N)
+    if (count > 1 and M and N and int(batch.get("stride_y", 0)) > 2 * M * N
+            and (write_y and y is None or quantize_out and q_out is None)):
+        raise ValueError("a batch with gaps between its outputs (stride_y) needs them given")
+    _need_cuda(a_q, a_sf, b, b_sf, bias, residual)
     if not write_y and not quantize_out:
         raise ValueError("write_y=False needs quantize_out=True")
     if y is None and write_y:

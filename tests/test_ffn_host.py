@@ -222,6 +222,27 @@ def test_batched_outputs_keep_apart(L):
             call(stride, y)
 
 
+@pytest.mark.parametrize("kind", [bq.W_MXFP4, bq.W_FP8BLK32, bq.W_MXFP8, bq.W_A4W4, bq.W_GRAD,
+                                  bq.W_NVFP4])
+def test_block_scaled_batch_with_gaps_needs_its_outputs(kind):
+    """The tensors made for a batch's outputs have no room for gaps."""
+    M, N, K, count = 4, 32, 128, 2
+    u8 = torch.zeros(1 << 16, dtype=torch.uint8)
+    y, q = torch.zeros(1024, dtype=torch.bfloat16), torch.zeros(1024, dtype=torch.uint8)
+
+    def call(stride_y, **kw):
+        bq.gemm(kind, u8, u8, u8, u8, M, N, K, batch=dict(count=count, stride_y=stride_y), **kw)
+    gaps = 2 * M * N + 64
+    for kw in (dict(), dict(quantize_out=True, y=y), dict(quantize_out=True, write_y=False),
+               dict(quantize_out=True, q_out=q)):
+        with pytest.raises(ValueError, match="needs them given"):
+            call(gaps, **kw)
+    for stride, kw in ((2 * M * N, {}), (gaps, dict(y=y)),
+                       (gaps, dict(quantize_out=True, y=y, q_out=q))):
+        with pytest.raises(ValueError, match="CUDA tensors only"):
+            call(stride, **kw)
+
+
 def test_plans():
     def p(M, N, K, **kw):
         c = bq.ffn_plan(M, N, K, **kw)
