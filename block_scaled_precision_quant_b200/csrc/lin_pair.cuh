@@ -220,10 +220,8 @@ __global__ void __launch_bounds__(kLinPairThreads, 1)
   if (warp == 0 || warp == 2) {
     // -------------------------------------------------------- tile copies --
     if (lane == 0) {
-      if (warp == 0) {  // the activations may come from the kernel before
-        griddep_wait();
-        griddep_launch_dependents();
-      }
+      griddep_wait();  // both operands may come from the kernel before
+      if (warp == 0) griddep_launch_dependents();
       const uint32_t tx = warp == 0 ? 2 * L::kBytesA : 2 * a.w_tile_bytes;
       int stage = 0;
       uint32_t phase = 0;

@@ -19,6 +19,11 @@
 // began at row 32 of an atom would have to name its scales by an odd TMEM
 // column, which the MMA does not take.
 //
+// MX weights are read ahead of the kernel before, which by the library's rule has not
+// written them.  Int8 weights are not: the quantizer of activations is theirs too, and
+// may well come last before the product.  (Reading them ahead took 0.1 us off a chain of
+// one-token products of 4.4, 0.2 off 41 x 4608 x 1536, 1.3 off 16 x 16384 x 8192 of 26.5.)
+//
 // What bounds it: the weights are read once per BN rows, so HBM for large
 // weights, and for small ones the chain launch - first copies - MMAs - exchange.
 // Measured: gated FP8 16 x 16384 x 8192 (277 MB) 46 us, 6.0 TB/s, 94 % of the copy
@@ -145,9 +150,9 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
     tma_prefetch_desc(&tm_w0);
     tma_prefetch_desc(&tm_a);
     if (GATED) tma_prefetch_desc(&tm_w1);
-    // The first weight tiles do not wait for the kernel before, nor for the
+    // The first MX weight tiles do not wait for the kernel before, nor for the
     // set-up that follows.
-    for (int st = 0; st < kStages && kt0 + st < kt1; ++st) {
+    for (int st = 0; !I8 && st < kStages && kt0 + st < kt1; ++st) {
       mbar_arrive_expect_tx(&full[st], a.w_tile_bytes);
       tma_load_3d(smem + st * L::kStageTiles, &tm_w0, &full[st], (kt0 + st) * kBlockK, n0,
                   a.p_batched ? b : 0);
@@ -163,16 +168,14 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
                       (GATED && warp == 9);
   if (copier) {
     if (lane == 0) {
-      const bool act = warp == 6 || warp == 8;
-      if (act) {
-        griddep_wait();
-        if (warp == 6) griddep_launch_dependents();
-      }
+      // int8 weights may come from the kernel before as well as the activations
+      if (I8 || warp == 6 || warp == 8) griddep_wait();
+      if (warp == 6) griddep_launch_dependents();
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       int kt = kt0;
-      if (warp == 0) {  // the tiles issued above
+      if (!I8 && warp == 0) {  // the tiles issued above
         kt = min(kt0 + kStages, kt1);
         phase = 1;
       }

@@ -525,8 +525,9 @@ int bq_act_quant_int8(const void *x_bf16, int64_t M, int64_t K, int64_t ldx, voi
  * with bq_epilogue's options except the quantized output (BQ_ERR_INVALID), and
  * bq_batch (its scale strides step the fp32 scales: bytes, multiples of 4 for
  * a_scale, of 16 for b_scale; stride_y is at least 2 M N, so that outputs do not
- * overlap, else BQ_ERR_SHAPE).  It needs no workspace.  Stream order as the
- * GEMMs above: b may be read early (a_scale, b_scale, bias and residual are not).
+ * overlap, else BQ_ERR_SHAPE).  It needs no workspace.  Stream order: unlike the
+ * GEMMs above it reads no operand, b neither, before the kernel before it has
+ * ended: a weight may be quantized right before the product.
  * M, N <= 0x7FFFFE00 (here and in bq_gemm_gated).
  * Schedules (bq_gemm_config): swap_ab 1: block_n 32, 64 or 128 activation rows
  * per tile, split_k 1 .. 8 CTAs of a cluster (split_mode AUTO or CLUSTER);
@@ -569,8 +570,9 @@ typedef struct {
  *   b_gate, b_up [N, K] weights; h_bf16 [M, N] out, N % 8 == 0, 16-byte aligned
  *   epi NULL: alpha 1, SiLU, no further outputs.
  * Schedules as bq_gemm_int8_int8, but MX tiles of 32 or 64 rows hold all M rows
- * (else BQ_ERR_INVALID).  Stream order as the GEMMs above: both weights
- * (and MX weight scales) may be read early.  A NaN or Inf in a quantized h is
+ * (else BQ_ERR_INVALID).  Stream order: MX weights and their scales may be read
+ * early, as in the GEMMs above, and must not be written by the kernel issued
+ * immediately before; int8 weights are not (bq_gemm_int8_int8).  A NaN or Inf in a quantized h is
  * reported by bq_device_status.
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_INVALID (kind, act,
  * schedule), BQ_ERR_ARCH, BQ_ERR_CUDA. */

@@ -398,3 +398,44 @@ def test_arch_override_refuses():
         assert e.value.status == bq.BQ_ERR_ARCH
     finally:
         bq.lib().bq_debug_override_compute_capability(-1, -1)
+
+
+@pytest.mark.parametrize("M,N,K,config", [
+    (1, 4608, 1536, {}), (41, 1536, 6144, {}), (41, 1000, 1040, dict(split_k=1, block_n=64)),
+    (130, 2048, 1024, dict(swap_ab=1, block_n=128)), (70, 4096, 512, dict(swap_ab=0)),
+    (1000, 4104, 2064, dict(swap_ab=0))])
+@pytest.mark.parametrize("gated", [False, True])
+def test_weights_quantized_right_before_in_every_schedule(M, N, K, config, gated):
+    """Products read their weights after the kernel before has ended: each call's weights
+    are written by the kernel just before it, into the buffers that the last call's used, in
+    eager order and replayed."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    x = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+    ws = [torch.randn((N, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    xq, xs = bq.act_quant_int8(x)
+    cfg = bq.config(**config)
+    b, sb = torch.empty((N, K), dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+    ug, us = bq.act_quant_int8(ws[0])  # the other weight of a gated block
+
+    def call(w, wait):
+        bq.act_quant_int8(w, b, sb)
+        if wait:
+            torch.cuda.synchronize()
+        if gated:  # written last: the up projection's weight
+            return bq.gemm_gated(bq.W_INT8, xq, xs, ug, us, b, sb, M, N, K, config=cfg)
+        return bq.gemm_int8_int8(xq, xs, b, sb, M, N, K, config=cfg)
+
+    want = [call(w, True) for w in ws]
+    assert not torch.equal(want[0], want[1])
+    for _ in range(10):
+        got = [call(w, False) for w in ws]
+        assert all(torch.equal(a, e) for a, e in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [call(w, False) for w in ws]
+    for _ in range(10):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, e) for a, e in zip(got, want))
+    bq.device_status()
