@@ -12,11 +12,14 @@
 // else does.  Then an addition's own round to nearest even decides.  The
 // floor of amax is a power of two so that A stays short.
 //
-// Reads 2 bytes and writes 1 an element; HBM bounds it: 8192 x 8192 31.1 us, 6.5 TB/s,
+// Reads 2 bytes and writes 1 an element; HBM bounds it: 8192 x 8192 30.5 us, 6.6 TB/s,
 // the copy rate.
 //
-// The next kernel starts when this one has ended (41 x 1536: 1.4 us; int8 products wait
-// for that before they read either operand).
+// The next kernel may start early: int8 products, whose weight these codes may be, wait
+// for this one's end before they read either operand.  A product behind it gains 0.3 to 1
+// us (both kernels: 41 x 4608 x 1536 7.6 to 7.2 us, 512 x 4096 x 4096 18.1 to 17.2), a chain
+// of long quantizers as well (4096 x 4096 10.3 to 10.1 us, 8192 x 8192 31.1 to 30.5); alone
+// and tiny it takes 0.1 longer (41 x 1536: 1.4 and 1.5 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -61,6 +64,7 @@ __global__ void __launch_bounds__(256) i8_quant_warp_kernel(const __nv_bfloat16 
   const int lane = threadIdx.x & 31;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   griddep_wait();
+  griddep_launch_dependents();
   if (m >= M) return;  // whole warps leave
   const uint4 *src = reinterpret_cast<const uint4 *>(x + m * ldx);
   const int nv = static_cast<int>(K / 8);
@@ -104,6 +108,7 @@ __global__ void __launch_bounds__(THREADS) i8_quant_kernel(const __nv_bfloat16 *
                                                            int *__restrict__ status) {
   __shared__ uint32_t part[THREADS / 32];
   griddep_wait();
+  griddep_launch_dependents();
   const int64_t m = blockIdx.x;
   const uint4 *src = reinterpret_cast<const uint4 *>(x + m * ldx);
   const int64_t nv = K / 8;
