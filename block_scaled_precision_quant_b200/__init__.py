@@ -6,7 +6,9 @@ capability 10.0 (B200); torch is used for device memory, streams and the
 optional allocation of outputs.  If ``libbq.so`` has not been built, the first
 call raises -- there is no CPU fallback.
 
-Build the library with ``python -m block_scaled_precision_quant_b200.build``.
+Build the library with ``python -m block_scaled_precision_quant_b200.build``.  The calls of the
+int8 and gated operators also need the compiled module that it builds with g++ and torch's
+headers (_torch_calls.so); the other calls do without.
 """
 from __future__ import annotations
 

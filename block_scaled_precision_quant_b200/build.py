@@ -9,6 +9,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -63,6 +64,8 @@ def build_calls(force: bool = False):
         return CALLS
     torch_dir = os.path.dirname(spec.origin)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
+    if os.path.exists(CALLS):  # of other sources: not to be loaded should this build fail
+        os.remove(CALLS)
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
            "-fvisibility=hidden", "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
@@ -79,7 +82,15 @@ def build_calls(force: bool = False):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_calls(force)
+    build_lib(force, verbose)
+    try:
+        build_calls(force)
+    except (RuntimeError, OSError) as e:  # the library does without; what needs them says so
+        warnings.warn(f"the binding's compiled calls are not built: {e}")
+    return LIB
+
+
+def build_lib(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
