@@ -604,11 +604,14 @@ def _load_native():
     if _native is None:
         _torch()
         L = lib()
+        from . import build
+        how = "build them with `python -m block_scaled_precision_quant_b200.build`"
+        if build.calls_built_for() not in (None, build.built_for()):
+            raise RuntimeError(f"the compiled calls are not built for {build.built_for()}: {how}")
         try:
             from . import _torch_calls as m
         except ImportError as e:
-            raise RuntimeError("the compiled calls are missing: build them with "
-                               "`python -m block_scaled_precision_quant_b200.build`") from e
+            raise RuntimeError(f"the compiled calls are missing: {how}") from e
         m.init(BqError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.bq_act_quant_int8, L.bq_gemm_int8_int8_epilogue, L.bq_gemm_gated,
             L.bq_gated_grad_quant)))

@@ -3,7 +3,9 @@ sm_100a, and, where torch is installed, the binding's compiled calls on torch te
 (_torch_calls.so).  Usage: python -m block_scaled_precision_quant_b200.build [--force]"""
 from __future__ import annotations
 
+import contextlib
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbq.so")
 CALLS = os.path.join(PKG, "_torch_calls.so")
+CALLS_STAMP = os.path.join(PKG, "_torch_calls.built")
 CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 
 NVCC_FLAGS = [
@@ -55,17 +58,36 @@ def up_to_date() -> bool:
     return current(LIB, deps())
 
 
+def built_for() -> str:
+    """The interpreter and the torch whose C++ interfaces the compiled calls are built against."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "?"
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch}"
+
+
+def calls_built_for():
+    """built_for() of the build of the compiled calls at hand, None if it is not known."""
+    try:
+        with open(CALLS_STAMP) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def build_calls(force: bool = False):
     """The extension module of csrc/torch_calls.cpp (g++), or None without torch."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.origin:
         return None
-    if not force and current(CALLS, [CALLS_SOURCE, os.path.join(INCLUDE, "bq.h")]):
+    if (not force and calls_built_for() == built_for()
+            and current(CALLS, [CALLS_SOURCE, os.path.join(INCLUDE, "bq.h")])):
         return CALLS
     torch_dir = os.path.dirname(spec.origin)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
-    if os.path.exists(CALLS):  # of other sources: not to be loaded should this build fail
-        os.remove(CALLS)
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(CALLS)  # of other sources: not to be loaded should this build fail
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
            "-fvisibility=hidden", "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
@@ -78,6 +100,8 @@ def build_calls(force: bool = False):
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("g++ failed building _torch_calls.so")
     os.replace(tmp, CALLS)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(built_for())
     return CALLS
 
 
