@@ -281,6 +281,15 @@ def test_plans():
             bq.ffn_plan(41, 4608, 1536, weight_kind=kind, gated=gate)
 
 
+def test_plans_of_large_weights_fill_the_device():
+    """Products that read their weights once keep at least 85 % of the SMs streaming."""
+    for M, N, K in ((1, 16384, 8192), (16, 16384, 8192), (41, 18944, 4096)):
+        for kw in (dict(), dict(gated=True), dict(gated=True, weight_kind=bq.W_FP8BLK32)):
+            c = bq.ffn_plan(M, N, K, **kw)
+            assert (c.swap_ab, c.block_n) == (1, 32 if M <= 32 else 64)
+            assert N // 128 * c.split_k >= 0.85 * 148
+
+
 def test_block_scaled_gemm_refuses_a_second_32_row_tile():
     """32-row decode tiles hold all activation rows: a second one would begin in the
     middle of a scale atom."""

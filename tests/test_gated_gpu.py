@@ -385,3 +385,42 @@ def test_empty_calls():
     e = torch.empty((0, 32), dtype=torch.bfloat16, device="cuda")
     out = bq.gated_grad_quant(e, torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"))
     assert out[0].shape == (0, 64)
+
+
+# the nearest form's sizes, and: more columns of F than a block's eight warps hold, a half tile
+# of 32 behind them, rows and groups of padding in every number
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N", [(32, 32), (32, 64), (64, 96), (96, 160), (128, 128), (160, 544),
+                                 (512, 1056), (1024, 2048), (224, 512), (32, 4128)])
+def test_grad_quant_stochastic_sizes(M, N, act):
+    dh, gu = grads(M, N, M + N)
+    d = torch.empty((M, 2 * N), dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = bq.gated_grad_quant(dh, gu, act=act, stochastic=True, seed=M * N, d=d, status=st)
+    ref, tol = grad_ref(dh, gu, act)
+    close(d, ref, tol, f"d {M}x{N}")
+    assert int(st) == 0
+    for x, y in zip(got, bq.grad_quant_dual(d, stochastic=True, seed=M * N)):
+        assert torch.equal(x, y)  # codes and scales, padding included
+
+
+def test_grad_quant_stochastic_strides_outputs_and_status():
+    M, N = 96, 288
+    dh, gu = grads(M, N + 64, 7)
+    a, b = dh[:, 16:16 + N], gu[:, 8:8 + 2 * N]
+    ref = bq.gated_grad_quant(a.contiguous(), b.contiguous(), stochastic=True, seed=5)
+    # buffers that hold other values, with more behind them
+    out = [torch.full((t.numel() + 64,), 77, dtype=torch.uint8, device="cuda") for t in ref]
+    got = bq.gated_grad_quant(a, b, stochastic=True, seed=5, out=out)
+    for x, y in zip(got, ref):
+        assert torch.equal(x[:y.numel()], y.reshape(-1)) and bool((x[y.numel():] == 77).all())
+    other = bq.gated_grad_quant(a, b, stochastic=True, seed=6)
+    assert not torch.equal(other[0], ref[0]) and torch.equal(other[1], ref[1])
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for value in (float("inf"), float("nan")):
+        for r, c in ((M - 1, N - 1), (0, 0), (33, 257)):
+            bad = a.contiguous()
+            bad[r, c] = value
+            st.zero_()
+            bq.gated_grad_quant(bad, b, stochastic=True, status=st)
+            assert int(st) == 1, (value, r, c)
