@@ -424,3 +424,51 @@ def test_grad_quant_stochastic_strides_outputs_and_status():
             st.zero_()
             bq.gated_grad_quant(bad, b, stochastic=True, status=st)
             assert int(st) == 1, (value, r, c)
+
+
+@pytest.mark.parametrize("kind", ["mxfp8", "int8"])
+def test_offsets_beyond_32_bits(kind):
+    """More than 2^31 hidden values and 2^32 projections: the last rows equal those of a
+    short call, forward and backward."""
+    M, N, K = 65568, 32800, 32
+    a = Operand("int8" if kind == "int8" else "mxfp8", M, K, 1)
+    w, v = Operand(kind, N, K, 2), Operand(kind, N, K, 3)
+    last = torch.arange(M - 32, M)  # a scale atom's last 32 rows
+    aq = a.q[M - 32:].contiguous()
+    if kind == "int8":
+        asf = a.sf[M - 32:].clone()
+    else:
+        s = bq.unpack_scales(a.sf, M, K)[last.cuda()]
+        asf = torch.full((bq.sf_bytes(32, K),), 127, dtype=torch.uint8, device="cuda")
+        asf.view(32, 4, 4)[:, 0, 0] = s[:, 0]
+    for cfg in (bq.config(swap_ab=0), bq.config(swap_ab=1, block_n=128)):
+        h, q, sf, gu = bq.gemm_gated(KIND[kind], a.q, a.sf, w.q, w.sf, v.q, v.sf, M, N, K,
+                                     alpha=0.01, keep_projections=True, quantize_out=True,
+                                     config=cfg)
+        bq.device_status()
+        e = bq.gemm_gated(KIND[kind], aq, asf, w.q, w.sf, v.q, v.sf, 32, N, K, alpha=0.01,
+                          keep_projections=True, quantize_out=True)
+        assert torch.equal(gu[-32:], e[3]) and torch.equal(h[-32:], e[0])
+        assert torch.equal(q[-32:], e[1])
+        got = bq.unpack_scales(sf, M, N)[-32:]
+        assert torch.equal(got, bq.unpack_scales(e[2], 32, N))
+        del h, q, sf
+    dh = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    dh[-32:], _ = grads(32, N, 5)
+    for stochastic in (False, True):
+        d_row, d_sf, d_t, d_tsf = bq.gated_grad_quant(dh, gu, stochastic=stochastic)
+        # nearest: the last 32 rows alone give the same codes, and so do their columns
+        if not stochastic:
+            e = bq.gated_grad_quant(dh[-32:], gu[-32:])
+            assert torch.equal(d_row[-32:], e[0]) and torch.equal(d_t[:, -32:], e[2])
+            assert torch.equal(bq.unpack_scales(d_sf, M, 2 * N)[-32:],
+                               bq.unpack_scales(e[1], 32, 2 * N))
+            assert torch.equal(bq.unpack_scales(d_tsf, 2 * N, M)[:, -1:],
+                               bq.unpack_scales(e[3], 2 * N, 32))
+        else:
+            d = torch.empty_like(gu)
+            got = bq.gated_grad_quant(dh, gu, stochastic=True, out=(d_row, d_sf, d_t, d_tsf), d=d)
+            for x, y in zip(bq.grad_quant_dual(d, stochastic=True), got):
+                assert torch.equal(x, y)
+        del d_row, d_t
+    bq.device_status()

@@ -439,3 +439,29 @@ def test_weights_quantized_right_before_in_every_schedule(M, N, K, config, gated
         graph.replay()
         assert all(torch.equal(a, e) for a, e in zip(got, want))
     bq.device_status()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements in the rows, the outputs and the residual: the last rows equal
+    those of a short call."""
+    M, K = 70001, 32768
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = rows(3, K, 1)
+    q, s = bq.act_quant_int8(x)
+    check_quant(x[-3:], q[-3:], s[-3:])
+    assert int(q[-4].abs().max()) == 0
+    del x, q, s
+    N, K = 32768, 16
+    a, b = Operand("int8", M, K, 2), Operand("int8", N, K, 3)
+    res = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    res[-5:] = rows(5, N, 4)
+    for cfg in (bq.config(swap_ab=0), bq.config(swap_ab=1, block_n=128)):
+        for r in (None, res):
+            y = bq.gemm_int8_int8(a.q, a.sf, b.q, b.sf, M, N, K, residual=r, config=cfg)
+            for first in (0, 65535, M - 5):  # 65535 N: around 2^31
+                t = slice(first, first + 5)
+                e = bq.gemm_int8_int8(a.q[t].contiguous(), a.sf[t].clone(), b.q, b.sf, 5, N, K,
+                                      residual=None if r is None else r[t])
+                assert torch.equal(y[t], e)
+            del y
+    bq.device_status()
