@@ -337,7 +337,6 @@ void operand_args(const Call& c, bq::FfnArgs* g) {
   g->K = static_cast<int>(c.K);
   g->batch = static_cast<int>(c.batch.count);
   g->sf_katoms = static_cast<int>(ceil_div(c.K, 128));
-  g->sf_a_bands = static_cast<int>(ceil_div(c.M, 128));
   g->w_tile_bytes = 128 * 128 / (c.kind == kMxfp4 ? 2 : 1);
   g->fmt_a = bq::kFmtE4M3;
   g->fmt_w = c.kind == kMxfp4 ? bq::kFmtE2M1 : bq::kFmtE4M3;

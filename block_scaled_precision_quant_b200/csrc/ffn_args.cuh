@@ -28,7 +28,6 @@ struct FfnArgs : GemmArgs {
   uint32_t fmt_w, fmt_a;   // kind::mxf8f6f4 operand formats
   const uint8_t *sf_a;     // MX: scale atoms of A and of the weights
   const uint8_t *sf_w[2];
-  int sf_a_bands;          // 128-row bands of A's scale buffer
   const float *sa;         // int8: token scales [M] and channel scales [N]
   const float *sw[2];
   int64_t sa_bstride, sw_bstride;  // elements
@@ -66,8 +65,10 @@ __device__ __forceinline__ float exp2_fast(float x) {  // relative error 2^-22
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// g / (1 + e^-g): relative error near 2^-20 (half a bf16 step is 2^-8).  Below
-// g = -87 the quotient, under 2^-118, comes out as -0.
+// g / (1 + e^-g).  Relative error at most |g| 2^-23.7 for g < 0 (the exponent's argument
+// rounds: 2^-21 at -6, 2^-19 at -30, 2^-17.3 at -87) and 2^-21 of the two fast operations,
+// for any g above -87; half a bf16 step is 2^-8.  Below that the quotient, under 2^-118,
+// comes out as -0.
 __device__ __forceinline__ float silu(float g) {
   return g * rcp_fast(1.0f + exp2_fast(-kLog2e * g));
 }
