@@ -466,7 +466,10 @@ def gemm(weight_kind, a_q, a_sf, b, b_sf, M, N, K, y=None, bias=None, residual=N
     quantize_out: also return y quantized for the next GEMM (E4M3 codes
     [.., M, N] u8 and MMA-layout scales, exactly act_quant of y, written to
     q_out / sf_out when given); then returns (y or None, q, sf), with no bf16
-    y written when write_y is False."""
+    y written when write_y is False.
+    b and b_sf may be read while the kernel issued just before on the stream still runs:
+    quantize (or pack) them before the activations, not right before the product.  (Int8
+    weights may come last.)"""
     if weight_kind == W_INT8:
         if quantize_out or not write_y:
             raise ValueError("the int8 product has no quantized output")
@@ -646,7 +649,9 @@ def gemm_int8_int8(a_q, a_scale, b, b_scale, M, N, K, y=None, bias=None, residua
     """y = bf16(act(alpha * a_scale[m] * b_scale[n] * (A B^T) + bias) + residual) of
     int8 codes a_q [.., M, K] and b [.., N, K] with fp32 scales per token and per
     output channel (act_quant_int8).  batch: as in gemm; its scale strides
-    step the fp32 scales.  config: GemmConfig or None (auto)."""
+    step the fp32 scales, and outputs with gaps between them (stride_y) go to a given
+    y.  config: GemmConfig or None (auto).  Operands are read when the kernel before has
+    ended: either may be quantized last."""
     if batch is not None:
         batch = (int(batch["count"]), *(int(batch.get(k, 0)) for k in (
             "stride_a", "stride_a_sf", "stride_b", "stride_b_sf", "stride_y", "stride_res")))
@@ -665,7 +670,9 @@ def gemm_gated(weight_kind, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, M, N, K, y=
     [N, K].  keep_projections (or gu given): also return [g | u] bf16 [M, 2 N] for
     gated_grad_quant.  quantize_out: also return h quantized for the down
     projection (E4M3 codes and MMA-layout scales, exactly act_quant of h); no bf16
-    h is written when write_y is False.  Returns h, or a tuple (h or None, [q, sf],
+    h is written when write_y is False.  MX weights and their scales may be read while the
+    kernel issued just before still runs, as in gemm: quantize both weights before the
+    activations (int8 ones may come last).  Returns h, or a tuple (h or None, [q, sf],
     [gu]) when quantize_out or keep_projections ask for more."""
     y, q, sf, gu = (_native or _load_native()).gemm_gated(
         weight_kind, a_q, a_sf, b_gate, gate_sf, b_up, up_sf, M, N, K, y, act, alpha,
@@ -679,7 +686,8 @@ def gated_grad_quant(dh, gu, act=BQ_GATE_SILU, stochastic=False, seed=0, out=Non
                      status=None):
     """Backward pass of h = act(g) * u: d = [dh * u * act'(g) | dh * act(g)] [M, 2 N]
     from dh bf16 [M, N] and gu = [g | u] bf16 [M, 2 N], quantized to E5M2 along
-    both dimensions as grad_quant_dual(d) does.  Returns (q_row [M, 2 N], sf_row, q_t
+    both dimensions as grad_quant_dual(d) does.  g and u hold the forward call's alpha: the
+    products of d with the input and with the weights take it once more (alpha=).  Returns (q_row [M, 2 N], sf_row, q_t
     [2 N, M], sf_t); d (bf16 [M, 2 N]) is written when given."""
     q_row, sf_row, q_t, sf_t = (None,) * 4 if out is None else out
     return (_native or _load_native()).gated_grad_quant(

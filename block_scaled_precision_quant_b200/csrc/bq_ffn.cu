@@ -160,11 +160,12 @@ int check_config(const bq_gemm_config* cfg) {
 
 // Estimated microseconds of the two schedules, fitted to 260 random problems of 1 to
 // 1500 rows, 256 to 16384 outputs and K of 256 to 8192, each measured in every
-// schedule (a mean of 10 % off; the schedules picked take 1.3 % more than the best).
+// schedule (a mean of 10 % off; the schedules picked take 0.9 % more than the best, 34 % at
+// worst).
 //   swap: launch, first copies and outputs 3 us (MX 4.1), longer by the tile's rows.  A
 //         CTA fills its shared memory at 105 KB/us (packed weights at their unpacked
 //         size), all of them at 8.3 GB/ms from L2.  A split adds the exchange (int8 41
-//         x 4608 x 1536: 6.4 us unsplit, 5.4 in 4 slices; 41 x 1536 x 6144: 14.5 and 5.6
+//         x 4608 x 1536: 6.4 us unsplit, 5.5 in 2 slices; 41 x 1536 x 6144: 14.8 and 5.5
 //         in 8; gated MXFP4 41 x 6144 x 1536: 10.4 and 8.5 in 2 or 4), more CTAs than SMs
 //         their start.
 //   pair: 5.1 us and 0.26 us (MX 0.33) a K block of 256 x 256 (int8 256 x 4096 x 4096:

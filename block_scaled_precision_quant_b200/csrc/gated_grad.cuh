@@ -151,8 +151,11 @@ __device__ __forceinline__ void dual_quant_tile(const uint32_t (&w)[32], int64_t
 // bf16, row pitch 2 F (optional).  R % 32 == 0, F % 32 == 0.
 // grid.x = 32-row group (up to the scale padding), grid.y * 8 + warp = tile of 64
 // columns of F; a warp forms and quantizes its tile of dG, then that of dU.
-// Bound by the random words' 64-bit multiplications (they are bq_grad_quant_dual's):
-// 4096 x 6144 300 us.
+// 4096 x 6144 300 us (bq_grad_quant_dual of a ready [4096, 12288] gradient 190): far from
+// memory's 36, and from the 113 that its instructions (79 an element of d, most of them the
+// random words' and both roundings') would take if one issued every cycle.  One issues in
+// 35 % of them: 16 warps an SM, at 128 registers a thread, run through two unrolled copies
+// of the tile's quantizer and wait for instructions most often, then for their own results.
 template <int ACT>
 __global__ void __launch_bounds__(256, 2) gated_grad_sr_kernel(
     const __nv_bfloat16 *__restrict__ dh, int64_t ld_dh, const __nv_bfloat16 *__restrict__ gu,
@@ -223,9 +226,10 @@ __global__ void __launch_bounds__(256, 2) gated_grad_sr_kernel(
 //   3. two columns x 32 rows a thread, whole groups: the transposed codes, which
 //      turn around through the tiles' memory and leave as 128-byte lines.
 // Floor: 6 bytes read and 4.1 written for each element of F.  Bound by the
-// instructions it issues (46 an element before pairs of values took one, 63 in a
-// version that kept one ownership and met by shuffles): 4096 x 6144 53 us, 4.8 TB/s
-// (GELU 59 to 66; bq_grad_quant_dual of a ready [4096, 12288] gradient 88).
+// instructions it issues (41 an element, in 60 % of the cycles; 46 before pairs of values
+// took one, 63 in a version that kept one ownership and met by shuffles) and the wait for
+// a block's tiles: 4096 x 6144 53 us, 4.8 TB/s (GELU 59 to 66; bq_grad_quant_dual of a
+// ready [4096, 12288] gradient 88).
 struct GradSmem {
   static constexpr int kTile = 128 * 256;         // [128 rows][128 bf16]: g, u, dH
   static constexpr int kOffSfr = 3 * kTile;       // [2][128 rows][4 groups]

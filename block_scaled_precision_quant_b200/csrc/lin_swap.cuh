@@ -22,13 +22,14 @@
 // MX weights are read ahead of the kernel before, which by the library's rule has not
 // written them.  Int8 weights are not: the quantizer of activations is theirs too, and
 // may well come last before the product.  (Reading them ahead took 0.1 us off a chain of
-// one-token products of 4.4, 0.2 off 41 x 4608 x 1536, 1.3 off 16 x 16384 x 8192 of 26.5.)
+// one-token products of 4.35, nothing off 41 x 4608 x 1536, 1.2 off 16 x 16384 x 8192 of
+// 26.2.)
 //
 // What bounds it: the weights are read once per BN rows, so HBM for large
 // weights, and for small ones the chain launch - first copies - MMAs - exchange.
 // Measured: gated FP8 16 x 16384 x 8192 (277 MB) 46 us, 6.0 TB/s, 94 % of the copy
 // rate; gated MXFP4 41 x 6144 x 1536 8.5 us (unsplit 10.4); int8 with a bias
-// 1 x 4608 x 1536 4.3 us (unsplit 5.3).
+// 1 x 4608 x 1536 4.35 us (unsplit 5.4).
 #pragma once
 
 #include "ffn_args.cuh"
@@ -262,8 +263,8 @@ __global__ void __launch_bounds__(kSwapThreads, OCC)
   // The scales, bias and residual may come from the preceding kernel, which
   // may also still read or write the outputs.
   griddep_wait();
-  // What the outputs need besides the sums, fetched while those are formed (int8 41 x
-  // 1536 x 6144: 7.0 us with the scales fetched behind the exchange, 6.6 so).
+  // What the outputs need besides the sums, fetched while those are formed (0.4 us of int8
+  // 41 x 1536 x 6144, whose scales came behind the exchange before).
   const int mt = min(BN, a.M - m0);
   const int n = n0 + 4 * lane;
   const bool nok = n < a.N;

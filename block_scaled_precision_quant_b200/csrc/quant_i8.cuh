@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(256) i8_quant_warp_kernel(const __nv_bfloat16 
 }
 
 // One block of THREADS per row.  Each thread keeps its first VECS 16-byte pieces; the
-// rest of a longer row is read twice, the second time from the caches.  256 threads
+// rest of a longer row is read twice, the second time from the caches.  (With 8 pieces the
+// compiler spills 16 bytes of a thread's.)  256 threads
 // of 4 pieces suit long rows, 128 of 8 many middling ones (8192 x 4112: 23.7 and
 // 19.0 us, 600 x 4096: 2.6 and 2.45; 200 x 2048: 1.67 and 1.71, 8192 x 8192: 31.1
 // and 31.9).

@@ -250,6 +250,7 @@ int bq_unpack_scales(const void *sf_mma, int64_t rows, int64_t K, void *rowmajor
  * scales, bias or residual and before writing y, but it may read the weight
  * operand b and b_sf early: they must not be written by the kernel issued
  * immediately before the GEMM on the same stream (anything older has finished).
+ * (The int8 products below wait before they read b, too.)
  * Once all its thread blocks are past that wait, a GEMM lets the next kernel
  * of the stream launch if that kernel was launched programmatically (as this
  * library's are); such a kernel waits for the GEMM before touching its output. */
@@ -593,7 +594,8 @@ int bq_ffn_plan(int weight_kind, int gated, int64_t M, int64_t N, int64_t K, int
  * quantizes a [M, 2 N] gradient (rounding, seed, q_row, sf_row, q_t, sf_t as
  * there).  With Wg and Wu stacked to W [2 N, K] the gradients are
  *   dX = bq_gemm_e5m2_mxfp8(q_row, bq_quant_transposed(W), M, K, 2 N)
- *   dW = bq_gemm_e5m2_mxfp8(q_t, bq_quant_transposed(X), 2 N, K, M).
+ *   dW = bq_gemm_e5m2_mxfp8(q_t, bq_quant_transposed(X), 2 N, K, M),
+ * times the forward call's alpha (bq_epilogue's alpha): G and U hold it already.
  *   dh_bf16 [M, N] (row stride ld_dh >= N), gu_bf16 [M, 2 N] as bq_gemm_gated
  *   keeps it (row stride ld_gu >= 2 N); M % 32 == 0, N % 32 == 0, strides % 8 == 0,
  *   bases 16-byte aligned; sf_row and sf_t 4-byte aligned

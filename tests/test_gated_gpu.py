@@ -495,3 +495,40 @@ def test_block_repeats_bit_for_bit(kind):
         block(a[1])
         assert all(torch.equal(x, y) for x, y in zip(first, block(a[0])))
     bq.device_status()
+
+
+@pytest.mark.parametrize("alpha", [0.5, -2.0])
+def test_gradients_take_alpha_once_more(alpha):
+    """g and u hold the forward call's alpha; the products of d with the input and with the
+    weights take it as well."""
+    M, N, K = 64, 96, 128
+    a, w, v = Operand("mxfp8", M, K, 1), Operand("mxfp8", N, K, 2), Operand("mxfp8", N, K, 3)
+    small = float(np.float32(alpha / float(product(a, w).std())))
+    _, gu = bq.gemm_gated(bq.W_MXFP8, a.q, a.sf, w.q, w.sf, v.q, v.sf, M, N, K, alpha=small,
+                          keep_projections=True)
+    g = torch.Generator().manual_seed(4)
+    dh = (torch.randn((M, N), generator=g) * 2.0 ** -6).to(torch.bfloat16).cuda()
+    d = torch.empty((M, 2 * N), dtype=torch.bfloat16, device="cuda")
+    q, sf, _, _ = bq.gated_grad_quant(dh, gu, d=d)
+    wt = torch.cat((w.value, v.value), 0)
+    wq = bq.quant_transposed(wt.to(torch.bfloat16))
+    dx = bq.gemm_e5m2_mxfp8(q, sf, *wq, M, K, 2 * N, alpha=small)
+    bq.device_status()
+    # autograd in 64 bits through the block's formula
+    x, wd, vd = a.value.clone().requires_grad_(), w.value, v.value
+    h = torch.nn.functional.silu(small * x @ wd.t()) * (small * x @ vd.t())
+    h.backward(dh.double())
+    # half steps: bf16's of g, u (each reaches d with a factor up to 1 + |g| or so, 10 here), of d
+    # and of the weights, E5M2's of d 2^-3, E4M3's of the weights 2^-4, over the sum's terms; codes
+    # below a group's smallest step: as in test_block_forward_and_backward
+    size = abs(small) * (d.double().abs() @ wt.abs())
+    rel = (1 + 2.0 ** -3 + 2.0 ** -7) * (1 + 2.0 ** -4 + 2.0 ** -8) - 1
+    forward = abs(small) * 10 * BF16 * (dh.double().abs() * (gu[:, :N].double().abs() + 1)
+                                        * (gu[:, N:].double().abs() + 1)) @ (w.value.abs()
+                                                                            + v.value.abs())
+    floor = abs(small) * (d.double().abs().amax() * 2.0 ** -31 * wt.abs().sum(0)
+                          + wt.abs().amax() * 2.0 ** -17 * d.double().abs().sum(1, keepdim=True))
+    close(dx, x.grad, size * rel + forward + floor + x.grad.abs() * BF16)
+    # the tolerance tells alpha from alpha squared: without the factor most values lie outside
+    off = (dx.double() / small - x.grad).abs() > (size * rel + forward + floor)
+    assert float(off.double().mean()) > 0.5
